@@ -354,6 +354,138 @@ size_t qat4_fq_gemm_staged_workspace_bytes(int64_t R, int64_t C);
 qat4_status qat4_fq_gemm_staged(const uint16_t *X, int64_t T, const float *W, const float *delta, int64_t R,
                                 int64_t C, float *Y, void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* ------------------------------------------------ 4-bit key/value cache
+ * Serving next to the W4A16 export: a paged key/value cache on the same kind of
+ * grid as the weights (model card "Opt.Gear-1B-qat-int4-per-channel-
+ * unquantized", section "Quantization Configuration": symmetric INT4, zero-
+ * point 0, 16-bit activations), its bookkeeping, and the attention that reads
+ * it.  The pages describe no cache format; this one is the library's own.
+ *
+ * A cache holds num_pages pages of page_size tokens of kv_heads heads of
+ * head_dim channels, keys and values alike:
+ *  k_codes, v_codes    uint8 [num_pages, kv_heads, page_size, head_dim / 2]:
+ *            channel 2j in the low nibble of byte j, 2j+1 in the high one
+ *            (4-bit two's complement, as qat4_pack_w4a16).
+ *  k_scales, v_scales  bf16 bit patterns [num_pages, kv_heads, page_size,
+ *            head_dim / 32]: one step size per 32 channels, as
+ *            qat4_kv4_append writes them: 5 significant bits, 0 or between
+ *            2^-100 and 2^100, so that step * code is exactly a bf16.  The
+ *            attention and gather calls round step * code of other steps to
+ *            bf16; steps that are negative, infinite or NaN give unspecified
+ *            values (never a fault).
+ *  page_size 16, 32, 64 or 128;  head_dim 64 or 128;  1 <= kv_heads <= 1024;
+ *  num_pages >= 1, num_pages * page_size <= 2^31 - 1.  All four pointers 16-byte
+ *  aligned.  The struct is read during the call only.
+ *
+ * Token slots and lengths are int32.  Slot s is token s % page_size of page
+ * s / page_size.  The int32 arrays of these calls need 4-byte alignment only.
+ * Their contents live on the device and cannot be checked on the host: the
+ * kernels bound every index they take from them, so wrong contents never read
+ * or write outside the given arrays, as each call states below. */
+typedef struct {
+    uint8_t *k_codes;
+    uint16_t *k_scales;
+    uint8_t *v_codes;
+    uint16_t *v_scales;
+    int64_t num_pages;
+    int32_t page_size, kv_heads, head_dim;
+} qat4_kv4_cache;
+
+/* Block tables and slot maps of one scheduling step, from request lengths.
+ *  lengths      int32 [B]: tokens each request holds already (0 for a new one).
+ *  new_lengths  int32 [B]: tokens it gets in this step (0 or more).  Negative
+ *               entries of either count as 0.
+ *  block_table  int32 [B, max_blocks], row stride table_stride >= max_blocks, in
+ *               place: entries [ceil(len/page_size), ceil((len+new)/page_size)) of
+ *               a row (cut at max_blocks) take the next pages of free_pages in
+ *               the order of the requests, or -1 when the list is used up; the
+ *               other entries stay as they are.
+ *  free_pages   int32 [num_free] (may be NULL when num_free is 0): unused pages.
+ *  seq_lens     out int32 [B]: len + new (not cut).
+ *  cu_new       out int32 [B + 1]: exclusive prefix sums of new_lengths.
+ *  slots        out int32 [num_slots]: the slot of each new token, requests one
+ *               after the other; -1 for a token without a page (table row or
+ *               free list too short) and for the entries past the last token.
+ *               Tokens past num_slots get no entry.
+ *  taken        out int32 [1]: pages wanted from free_pages (more than num_free
+ *               when the list was too short).
+ *  1 <= B <= 16384.  No two of the arrays may overlap.
+ *  Errors: QAT4_ERR_NULL, _SHAPE (sizes; a table row stride below max_blocks; an
+ *  output that overlaps lengths or new_lengths), _ALIGN, _CUDA. */
+qat4_status qat4_kv4_tables(const int32_t *lengths, const int32_t *new_lengths, int64_t B, int32_t *block_table,
+                            int64_t table_stride, int64_t max_blocks, const int32_t *free_pages, int64_t num_free,
+                            int32_t page_size, int32_t *seq_lens, int32_t *cu_new, int32_t *slots,
+                            int64_t num_slots, int32_t *taken, cudaStream_t stream);
+
+/* Quantizes keys and values and writes them to their slots.
+ *  k, v      [n, kv_heads, head_dim], bf16 bit patterns (QAT4_BF16) or float32
+ *            (QAT4_F32); head_dim contiguous, heads head_dim apart, tokens
+ *            k_stride and v_stride elements apart (at least kv_heads *
+ *            head_dim, a multiple of 16 bytes), so that they can be columns of
+ *            a stacked projection.
+ *  slots     int32 [n]: a token whose slot is negative or past the cache is
+ *            skipped.  Slots must be distinct: of two tokens with the same slot
+ *            any mixture may remain.
+ *  Per group of 32 channels with largest magnitude m: step = fl(m / 7) rounded
+ *  up to 5 significant bits, at most 2^100, and 0 where fl(m / 7) < 2^-100;
+ *  code = clamp(rint(fl(v / step)), -8, 7), and 0 where step is 0.  0 <= n.
+ *  A NaN is passed over for m and becomes code -8; an infinity gives the step
+ *  2^100.
+ *  Errors: QAT4_ERR_NULL, _SHAPE, _DTYPE, _ALIGN, _CUDA. */
+qat4_status qat4_kv4_append(const qat4_kv4_cache *cache, const void *k, const void *v, qat4_dtype dtype,
+                            int64_t k_stride, int64_t v_stride, const int32_t *slots, int64_t n,
+                            cudaStream_t stream);
+
+/* Reads tokens back: k, v out bf16 bit patterns [n, kv_heads, head_dim], the
+ * exact values step * code; zeros where the slot is negative or past the cache.
+ *  Errors: QAT4_ERR_NULL, _SHAPE, _ALIGN, _CUDA. */
+qat4_status qat4_kv4_gather(const qat4_kv4_cache *cache, const int32_t *slots, int64_t n, uint16_t *k, uint16_t *v,
+                            cudaStream_t stream);
+
+/* Softmax attention of a ragged batch of queries over the cache.
+ *  q         bf16 bit patterns [N, q_heads, head_dim]; head_dim contiguous, heads
+ *            head_dim apart, tokens q_stride elements apart (>= q_heads *
+ *            head_dim, a multiple of 8).  q_heads is a multiple of kv_heads (at
+ *            most 64 times); query head h reads head h / (q_heads / kv_heads).
+ *  cu_q      int32 [B + 1]: request b owns the query tokens [cu_q[b], cu_q[b+1]).
+ *            Tokens past cu_q[B] belong to none; their rows of out and lse stay
+ *            as they are.
+ *  seq_lens  int32 [B]: cached tokens of each request, this step's included.
+ *            The queries of a request are its last tokens: query j of nq has
+ *            position seq_len - nq + j.
+ *  block_table  int32 [B, max_blocks], row stride table_stride: the pages of each
+ *            request.  Lengths past max_blocks * page_size are cut there.
+ *            Tokens of an entry outside [0, num_pages) are left out, as if
+ *            masked; bytes of tokens past a request's length or before every
+ *            window are never used, whatever they hold.
+ *  scale     factor of q.k, > 0 and finite (normally 1/sqrt(head_dim)).
+ *  causal    1: a query sees the keys up to its own position; 0: all of its
+ *            request's.
+ *  window    0: no limit; w > 0 (causal only): the last w positions, its own
+ *            included.
+ *  out       bf16 bit patterns [N, q_heads, head_dim].  A query that sees no key
+ *            gives zeros.
+ *  lse       float32 [N, q_heads] (may be NULL): log of the sum of exp(scale q.k),
+ *            -infinity where no key is seen.
+ *  workspace device scratch of at least qat4_kv4_attention_workspace_bytes bytes,
+ *            16-byte aligned; contents on entry are ignored.  Calls that may
+ *            overlap on the GPU (other streams, two captured graphs) need one
+ *            each.
+ *  Keys and values enter exactly, products are exact, sums and statistics
+ *  float32; the softmax weights are rounded to bf16 for the second product
+ *  (their sum is not).  The result does not depend on timing (no atomics).
+ *  N >= 0; 1 <= B <= 65536; N * q_heads * head_dim <= 2^40, N * q_heads <= 2^31 - 1.
+ *  With cu_q not ascending inside [0, N], rows may be computed twice or not at
+ *  all; with scale * q.k overflowing float32 the row is unspecified.
+ *  Errors: QAT4_ERR_NULL, _SHAPE, _ALIGN, _WORKSPACE, _CUDA; a bounded wait that
+ *  gives up leaves QAT4_ERR_TIMEOUT for qat4_sync_check. */
+size_t qat4_kv4_attention_workspace_bytes(int64_t N, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+qat4_status qat4_kv4_attention(const uint16_t *q, int64_t q_stride, int64_t N, int64_t q_heads,
+                               const qat4_kv4_cache *cache, const int32_t *block_table, int64_t table_stride,
+                               int64_t max_blocks, const int32_t *seq_lens, const int32_t *cu_q, int64_t B,
+                               float scale, int32_t causal, int32_t window, uint16_t *out, float *lse,
+                               void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Synchronises `stream`, then reads and clears the library's device error
  * word for the current device.  Returns QAT4_ERR_TIMEOUT if a kernel gave up
  * a bounded wait since the last check, QAT4_ERR_CUDA if synchronisation

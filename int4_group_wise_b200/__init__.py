@@ -8,7 +8,8 @@ device pointers plus the current CUDA stream to the C ABI in
 
 Functions (same names as the C entry points, without the ``qat4_`` prefix):
 ``hessian``, ``hessian_workspace_bytes``, ``hessian_noalloc``, ``scale_search``, ``lsq_fwd``,
-``lsq_bwd``, ``lsq_fwd_bwd``, ``lsq_fwd_bwd_host``, ``pack_w4a16``, ``sync_check``,
+``lsq_bwd``, ``lsq_fwd_bwd``, ``lsq_fwd_bwd_host``, ``pack_w4a16``, ``kv4_tables``,
+``kv4_append``, ``kv4_gather``, ``kv4_attention`` (on a ``KV4Cache``), ``sync_check``,
 ``status_string``, ``selftest_bounded_wait``.
 """
 from __future__ import annotations
@@ -17,6 +18,7 @@ import ctypes as ct
 import math
 import os
 import struct
+from typing import NamedTuple
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqat4.so")
 
@@ -55,6 +57,12 @@ EXPORTS = {
     "qat4_fq_gemm_staged": (ct.c_int, [_P, _I64, _P, _P, _I64, _I64, _P, _P, ct.c_size_t, _P]),
     "qat4_refine_workspace_bytes": (ct.c_size_t, [_I64, _I64]),
     "qat4_refine": (ct.c_int, [_P, _I64, _I64, _P, _I64, _P, ct.c_int32, ct.c_int32, _P, _P, _P, _P, _Z, _P]),
+    "qat4_kv4_tables": (ct.c_int, [_P, _P, _I64, _P, _I64, _I64, _P, _I64, _I32, _P, _P, _P, _I64, _P, _P]),
+    "qat4_kv4_append": (ct.c_int, [_P, _P, _P, ct.c_int, _I64, _I64, _P, _I64, _P]),
+    "qat4_kv4_gather": (ct.c_int, [_P, _P, _I64, _P, _P, _P]),
+    "qat4_kv4_attention_workspace_bytes": (_Z, [_I64, _I64, _I64, _I64, _I64]),
+    "qat4_kv4_attention": (ct.c_int, [_P, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _F, _I32, _I32, _P, _P,
+                                      _P, _Z, _P]),
     "qat4_sync_check": (ct.c_int, [_P]),
     "qat4_selftest_bounded_wait": (ct.c_int, [_I64, _P]),
 }
@@ -480,6 +488,210 @@ def refine(W, H, alpha, idx, sweeps=1, delta=None, obj=None, workspace=None, str
                          _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream)),
            "qat4_refine")
     return delta, idx, obj
+
+
+# ------------------------------------------------------------------ 4-bit key/value cache
+class _CacheStruct(ct.Structure):
+    """qat4_kv4_cache of include/qat4.h."""
+    _fields_ = [("k_codes", _P), ("k_scales", _P), ("v_codes", _P), ("v_scales", _P), ("num_pages", _I64),
+                ("page_size", _I32), ("kv_heads", _I32), ("head_dim", _I32)]
+
+
+class KV4Cache(NamedTuple):
+    """A paged 4-bit key/value cache: codes uint8 [num_pages, kv_heads, page_size, head_dim / 2], step
+    sizes bfloat16 [num_pages, kv_heads, page_size, head_dim / 32].  The format is in include/qat4.h."""
+    k_codes: object
+    k_scales: object
+    v_codes: object
+    v_scales: object
+
+
+def kv4_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda") -> KV4Cache:
+    """An empty cache (all codes and step sizes 0)."""
+    import torch
+    if page_size not in (16, 32, 64, 128) or head_dim not in (64, 128) or kv_heads < 1 or num_pages < 1:
+        raise ValueError("page_size must be 16, 32, 64 or 128, head_dim 64 or 128, kv_heads and num_pages at least 1")
+    codes, scales = (num_pages, kv_heads, page_size, head_dim // 2), (num_pages, kv_heads, page_size, head_dim // 32)
+    return KV4Cache(*(torch.zeros(s, dtype=d, device=device)
+                      for _ in range(2) for s, d in ((codes, torch.uint8), (scales, torch.bfloat16))))
+
+
+def _cache_struct(cache):
+    import torch
+    kc = cache[0]
+    if not isinstance(kc, torch.Tensor) or kc.dim() != 4:
+        raise ValueError("k_codes must be [num_pages, kv_heads, page_size, head_dim / 2]")
+    n, h, p, half = kc.shape
+    scales = (n, h, p, half // 16)
+    return _CacheStruct(_dev(kc, "k_codes", torch.uint8), _dev(cache[1], "k_scales", torch.bfloat16, scales),
+                        _dev(cache[2], "v_codes", torch.uint8, kc.shape), _dev(cache[3], "v_scales", torch.bfloat16, scales),
+                        n, p, h, 2 * half)
+
+
+def _same_device(first, *others):
+    """The CUDA device that all tensors must share; the call is made with it current."""
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"all tensors must be on one device, got {first.device} and {t.device}")
+    return first.device
+
+
+class _on:
+    """Makes the tensors' device current for a call, and `stream` (when given) the current stream, so that
+    outputs and workspaces allocated inside belong to the stream that uses them."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.guards = []
+        if device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+            self.guards.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _rows3(t, name, heads, dim, dtypes):
+    """[n, heads, dim] whose rows may be strided (columns of a stacked projection)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [n, {heads}, {dim}], got {tuple(t.shape)}")
+    s = t.stride()
+    if t.numel() > 0 and ((dim > 1 and s[2] != 1) or (heads > 1 and s[1] != dim)):
+        raise ValueError(f"{name} must have contiguous heads and channels (strides [*, {dim}, 1]), got {s}")
+    return t.data_ptr(), (s[0] if t.shape[0] > 1 else heads * dim)
+
+
+def _table(t):
+    """A block table int32 [B, max_blocks] with contiguous rows (row stride of its own)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32:
+        raise TypeError("block_table must be an int32 CUDA tensor")
+    if t.dim() != 2 or t.shape[0] < 1 or t.shape[1] < 1 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("block_table must be [B, max_blocks] with contiguous rows")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def kv4_tables(lengths, new_lengths, block_table, free_pages, page_size, num_slots, seq_lens=None, cu_new=None,
+               slots=None, taken=None, stream=None):
+    """One scheduling step's bookkeeping on the device: gives each request the pages for its new tokens
+    (block_table int32 [B, max_blocks], updated in place from free_pages int32 [F]) and returns
+    (seq_lens int32 [B], cu_new int32 [B + 1], slots int32 [num_slots], taken int32 []).  lengths and
+    new_lengths are int32 [B]; num_slots is the room for new tokens (entries past the last are -1, which
+    kv4_append skips, so a padded batch can be captured in a graph).  taken > F means that the free list
+    was too short: the tokens without a page have slot -1."""
+    import torch
+    L = lib()
+    lp = _dev(lengths, "lengths", torch.int32)
+    if lengths.dim() != 1 or lengths.shape[0] < 1:
+        raise ValueError("lengths must be [B] with B >= 1")
+    B = lengths.shape[0]
+    np_ = _dev(new_lengths, "new_lengths", torch.int32, (B,))
+    tp, ts = _table(block_table)
+    if block_table.shape[0] != B:
+        raise ValueError(f"block_table must have {B} rows, got {block_table.shape[0]}")
+    fp = _dev(free_pages, "free_pages", torch.int32)
+    dev = _same_device(lengths, new_lengths, block_table, free_pages, seq_lens, cu_new, slots, taken)
+    num_slots, page_size = int(num_slots), int(page_size)
+    if num_slots < 0 or num_slots >= 1 << 31 or page_size not in (16, 32, 64, 128):
+        raise ValueError("num_slots must be in [0, 2^31), page_size 16, 32, 64 or 128")
+    with _on(dev, stream):
+        seq_lens = _out(seq_lens, "seq_lens", (B,), torch.int32, lengths)
+        cu_new = _out(cu_new, "cu_new", (B + 1,), torch.int32, lengths)
+        slots = _out(slots, "slots", (num_slots,), torch.int32, lengths)
+        taken = _out(taken, "taken", (), torch.int32, lengths)
+        _check(L.qat4_kv4_tables(lp, np_, B, tp, ts, block_table.shape[1], fp, free_pages.numel(), page_size,
+                                 seq_lens.data_ptr(), cu_new.data_ptr(), slots.data_ptr(), num_slots,
+                                 taken.data_ptr(), _stream(stream)), "qat4_kv4_tables")
+    return seq_lens, cu_new, slots, taken
+
+
+def kv4_append(cache, k, v, slots, stream=None):
+    """Quantizes k and v (bfloat16 or float32 [n, kv_heads, head_dim], rows may be strided) and writes
+    token i to slot slots[i] (int32 [n]) of the cache; negative slots are skipped."""
+    import torch
+    L = lib()
+    c = _cache_struct(cache)
+    kinds = (torch.bfloat16, torch.float32)
+    kp, ks = _rows3(k, "k", c.kv_heads, c.head_dim, kinds)
+    vp, vs = _rows3(v, "v", c.kv_heads, c.head_dim, (k.dtype,))
+    if v.shape[0] != k.shape[0]:
+        raise ValueError("k and v must have the same number of tokens")
+    sp = _dev(slots, "slots", torch.int32, (k.shape[0],))
+    with _on(_same_device(k, v, slots, *cache), stream):
+        _check(L.qat4_kv4_append(ct.byref(c), kp, vp, _gdtype(k), ks, vs, sp, k.shape[0], _stream(stream)),
+               "qat4_kv4_append")
+
+
+def kv4_gather(cache, slots, k=None, v=None, stream=None):
+    """The values of the tokens in slots (int32 [n]) as bfloat16 (k, v), each [n, kv_heads, head_dim];
+    zeros for negative slots."""
+    import torch
+    L = lib()
+    c = _cache_struct(cache)
+    sp = _dev(slots, "slots", torch.int32)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [n]")
+    shape = (slots.shape[0], c.kv_heads, c.head_dim)
+    with _on(_same_device(slots, k, v, *cache), stream):
+        k = _out(k, "k", shape, torch.bfloat16, slots)
+        v = _out(v, "v", shape, torch.bfloat16, slots)
+        _check(L.qat4_kv4_gather(ct.byref(c), sp, shape[0], k.data_ptr(), v.data_ptr(), _stream(stream)),
+               "qat4_kv4_gather")
+    return k, v
+
+
+def kv4_attention_workspace_bytes(N: int, B: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().qat4_kv4_attention_workspace_bytes(int(N), int(B), int(q_heads), int(kv_heads), int(head_dim)))
+
+
+def kv4_attention(q, cache, block_table, seq_lens, cu_q, scale=None, causal=True, window=0, out=None, lse=None,
+                  workspace=None, stream=None):
+    """Attention of a ragged batch over the cache: q bfloat16 [N, q_heads, head_dim] (rows may be
+    strided), request b owning the query tokens cu_q[b]..cu_q[b+1] (int32 [B + 1]), which are the last of
+    its seq_lens[b] (int32 [B]) cached tokens; block_table int32 [B, max_blocks].  Returns out bfloat16
+    [N, q_heads, head_dim]; pass lse (float32 [N, q_heads]) to get the log-sum-exp too.  scale defaults to
+    1/sqrt(head_dim); window > 0 limits each query to its last `window` positions.  Query rows past
+    cu_q[B] are not written."""
+    import torch
+    L = lib()
+    c = _cache_struct(cache)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [N, q_heads, head_dim]")
+    N, Hq = q.shape[0], q.shape[1]
+    if Hq < 1 or Hq % c.kv_heads != 0:
+        raise ValueError(f"q_heads ({Hq}) must be a multiple of kv_heads ({c.kv_heads})")
+    qp, qs = _rows3(q, "q", Hq, c.head_dim, (torch.bfloat16,))
+    tp, ts = _table(block_table)
+    B = block_table.shape[0]
+    lp = _dev(seq_lens, "seq_lens", torch.int32, (B,))
+    cp = _dev(cu_q, "cu_q", torch.int32, (B + 1,))
+    dev = _same_device(q, block_table, seq_lens, cu_q, out, lse, workspace, *cache)
+    scale = 1.0 / math.sqrt(c.head_dim) if scale is None else float(scale)
+    window = max(-1, min(int(window), 0x7fffffff))
+    with _on(dev, stream):
+        out = _out(out, "out", (N, Hq, c.head_dim), torch.bfloat16, q)
+        need = int(L.qat4_kv4_attention_workspace_bytes(N, B, Hq, c.kv_heads, c.head_dim))
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        _check(L.qat4_kv4_attention(qp, qs, N, Hq, ct.byref(c), tp, ts, block_table.shape[1], lp, cp, B, scale,
+                                    int(bool(causal)), window, out.data_ptr(),
+                                    _dev(lse, "lse", torch.float32, (N, Hq)) if lse is not None else None,
+                                    _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream)),
+               "qat4_kv4_attention")
+    return out
 
 
 def sync_check(stream=None):

@@ -1,0 +1,309 @@
+// kv4_cache.cuh -- the paged 4-bit key/value cache: its block tables and slot
+// maps, the quantizing writer and the reader back.
+//
+// Format (decode on the INT4 grid of the model card "Opt.Gear-1B-qat-int4-per-
+// channel-unquantized", section "Quantization Configuration": symmetric INT4,
+// zero-point 0, here with one step per 32 channels of a token's head): codes
+// uint8 [pages, heads, page, D/2] (channel 2j low nibble, 2j+1 high nibble, as
+// the W4A16 export), steps bf16 [pages, heads, page, D/32].  A step has 5
+// significant bits, so code * step (3 + 5 bits) is exactly a bf16: the
+// attention kernels feed the tensor cores with the cache's exact values.  The
+// step is fl(m / 7) rounded UP to those 5 bits (m the group's largest
+// magnitude), so no code is clipped; against an unrounded step the grid is up
+// to 1/16 (on average 1/32) coarser.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "device_common.cuh"
+
+namespace qat4 {
+
+// The device's view of a cache.
+struct Kv4View {
+    uint8_t* kc;
+    uint16_t* ks;
+    uint8_t* vc;
+    uint16_t* vs;
+    int64_t pages;
+    int page, heads, dim;
+};
+
+// ------------------------------------------------------------------ tables
+// One step's bookkeeping, from request lengths alone:
+//   have_b = ceil(len_b / P), need_b = ceil((len_b + new_b) / P), both at most
+//   max_blocks; entry i in [have_b, need_b) of request b takes
+//   free[sum_{b' < b} (need - have) + i - have_b], or -1 past the list's end;
+//   cu = prefix sums of new; slot of token tok of request b = page * P + pos % P
+//   with pos = len_b + tok - cu_b, or -1 where there is no page.
+// Every CTA scans all B requests itself into shared memory (B is small against
+// the tokens, and a second launch would cost more than the scan: 2-3 us), then
+// takes its share of the table rows and of the tokens.  A new token's page is
+// computed from the free list, not read from the table, so no CTA waits for
+// another's writes.  Bound by launch latency up to some ten thousand tokens,
+// then by the 4 bytes written per token.
+constexpr int kTbThreads = 512;
+constexpr int kTbMaxRequests = 16384;
+
+struct TablesParams {
+    const int* lengths;
+    const int* fresh;        // new tokens per request
+    int* table;
+    int64_t table_stride;
+    const int* free_pages;
+    int* seq_lens;
+    int* cu;
+    int* slots;
+    int* taken;
+    int64_t num_slots;
+    int B, max_blocks, num_free, page;
+    int vec;                 // slots is 16-byte aligned: four tokens leave in one store
+};
+
+__host__ __device__ constexpr size_t tables_smem_bytes(int B) {
+    return (2 * static_cast<size_t>(B) + 1) * 4;
+}
+
+__device__ __forceinline__ int tb_blocks(int64_t tokens, int page, int most) {
+    const int64_t n = (tokens + page - 1) / page;
+    return static_cast<int>(n < most ? n : most);
+}
+
+__global__ void __launch_bounds__(kTbThreads)
+kv4_tables_kernel(const TablesParams p) {
+    extern __shared__ int tb_smem[];
+    int* const cu = tb_smem;              // [B + 1]
+    int* const off = tb_smem + p.B + 1;   // [B] first free-list index of a request
+    __shared__ int64_t wsum[2][kTbThreads / 32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.B + kTbThreads - 1) / kTbThreads;
+    const int r0 = min(p.B, tid * per), r1 = min(p.B, r0 + per);
+
+    // sums of this thread's requests, then an exclusive scan over the block (64 bits: the totals of
+    // wrong lengths may pass 2^31, and are cut there)
+    int64_t n = 0, e = 0;
+    for (int b = r0; b < r1; ++b) {
+        const int len = max(0, p.lengths[b]), nw = max(0, p.fresh[b]);
+        n += nw;
+        e += tb_blocks(static_cast<int64_t>(len) + nw, p.page, p.max_blocks) - tb_blocks(len, p.page, p.max_blocks);
+    }
+    int64_t sn = n, se = e;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t a = __shfl_up_sync(0xffffffffu, sn, d), c = __shfl_up_sync(0xffffffffu, se, d);
+        if (lane >= d) { sn += a; se += c; }
+    }
+    if (lane == 31) { wsum[0][warp] = sn; wsum[1][warp] = se; }
+    __syncthreads();
+    int64_t bn = sn - n, be = se - e, tn = 0, te = 0;
+    for (int w = 0; w < kTbThreads / 32; ++w) {
+        if (w < warp) { bn += wsum[0][w]; be += wsum[1][w]; }
+        tn += wsum[0][w];
+        te += wsum[1][w];
+    }
+    const int64_t top = 0x7fffffff;
+    for (int b = r0; b < r1; ++b) {
+        const int len = max(0, p.lengths[b]), nw = max(0, p.fresh[b]);
+        cu[b] = static_cast<int>(bn < top ? bn : top);
+        off[b] = static_cast<int>(be < top ? be : top);
+        bn += nw;
+        be += tb_blocks(static_cast<int64_t>(len) + nw, p.page, p.max_blocks) - tb_blocks(len, p.page, p.max_blocks);
+    }
+    if (tid == 0) cu[p.B] = static_cast<int>(tn < top ? tn : top);
+    __syncthreads();
+
+    // lengths, offsets and table rows: a warp per request
+    if (blockIdx.x == 0) {
+        for (int b = tid; b <= p.B; b += kTbThreads) p.cu[b] = cu[b];
+        if (tid == 0) *p.taken = static_cast<int>(te < top ? te : top);
+    }
+    const int gwarp = blockIdx.x * (kTbThreads / 32) + warp, nwarps = gridDim.x * (kTbThreads / 32);
+    for (int b = gwarp; b < p.B; b += nwarps) {
+        const int len = max(0, p.lengths[b]);
+        const int64_t total = static_cast<int64_t>(len) + max(0, p.fresh[b]);
+        if (lane == 0) p.seq_lens[b] = static_cast<int>(total < top ? total : top);
+        const int have = tb_blocks(len, p.page, p.max_blocks), need = tb_blocks(total, p.page, p.max_blocks);
+        for (int i = have + lane; i < need; i += 32) {
+            const int64_t f = static_cast<int64_t>(off[b]) + i - have;
+            p.table[b * p.table_stride + i] = f < p.num_free ? p.free_pages[f] : -1;
+        }
+    }
+
+    // slots, four consecutive tokens per thread; the request of the first by binary search
+    const int sh = __ffs(p.page) - 1;
+    const int64_t count = cu[p.B];
+    for (int64_t t0 = 4 * (static_cast<int64_t>(blockIdx.x) * kTbThreads + tid); t0 < p.num_slots;
+         t0 += 4 * static_cast<int64_t>(gridDim.x) * kTbThreads) {
+        int out[4] = {-1, -1, -1, -1};
+        if (t0 < count) {
+            int lo = 0, hi = p.B;                      // cu[lo] <= t0 < cu[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (cu[mid] <= t0) lo = mid; else hi = mid;
+            }
+            int b = lo;
+            int len = max(0, p.lengths[b]), have = tb_blocks(len, p.page, p.max_blocks);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t tok = t0 + j;
+                if (tok >= count) break;
+                if (tok >= cu[b + 1]) {
+                    do { ++b; } while (tok >= cu[b + 1]);
+                    len = max(0, p.lengths[b]);
+                    have = tb_blocks(len, p.page, p.max_blocks);
+                }
+                const int64_t pos = static_cast<int64_t>(len) + tok - cu[b];
+                const int64_t blk = pos >> sh;
+                if (blk >= p.max_blocks) continue;
+                int64_t page = -1;
+                if (blk < have) {
+                    page = p.table[b * p.table_stride + blk];
+                } else {
+                    const int64_t f = off[b] + blk - have;
+                    if (f < p.num_free) page = p.free_pages[f];
+                }
+                const int64_t slot = (page << sh) + (pos & (p.page - 1));
+                if (page >= 0 && slot <= top) out[j] = static_cast<int>(slot);
+            }
+        }
+        if (p.vec && t0 + 4 <= p.num_slots) {
+            *reinterpret_cast<int4*>(p.slots + t0) = make_int4(out[0], out[1], out[2], out[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (t0 + j < p.num_slots) p.slots[t0 + j] = out[j];
+        }
+    }
+}
+
+// ------------------------------------------------------------------ append
+// Step of a group from its largest magnitude: fl(m / 7) with the 19 low of its
+// 23 stored significand bits rounded up (the carry moves into the exponent), at
+// most 2^100, and 0 below 2^-100 (then every code is 0).  The limits keep the
+// step, its reciprocal and 24 * step away from overflow and subnormals.
+__device__ __forceinline__ float kv4_step(float m) {
+    const float d = __fdiv_rn(m, 7.0f);
+    const float up = __uint_as_float((__float_as_uint(d) + 0x7FFFFu) & ~0x7FFFFu);
+    return d < 0x1p-100f ? 0.0f : fminf(up, 0x1p100f);
+}
+
+// Eight values as packed codes, two's-complement nibbles, value i at bits 4i.
+__device__ __forceinline__ uint32_t kv4_pack8(const float (&v)[8], float step) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float q = code_of(scaled_exact(v[i], step));
+        w |= (static_cast<uint32_t>(static_cast<int>(q)) & 15u) << (4 * i);
+    }
+    return w;
+}
+
+constexpr int kKvBlock = 256;
+
+// Thread = 8 channels of one token and head of k or v; four neighbouring lanes
+// hold a group and find its largest magnitude by two shuffles.  One pass: each
+// value is read once, codes leave as one 4-byte word per lane.
+template <bool BF16>
+__global__ void __launch_bounds__(kKvBlock)
+kv4_append_kernel(const Kv4View c, const void* __restrict__ k, const void* __restrict__ v, int64_t k_stride,
+                  int64_t v_stride, const int* __restrict__ slots, int64_t items) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kKvBlock + threadIdx.x;   // items is a multiple of 4
+    const bool in = i < 2 * items;
+    const bool isv = in && i >= items;
+    const int64_t u = in ? (isv ? i - items : i) : 0;
+    const int words = c.dim >> 3;                           // 8-channel words of a head
+    const int row = c.heads * words;
+    const int64_t tok = u / row;
+    const int rest = static_cast<int>(u - tok * row);
+    const int head = rest / words, w = rest - head * words;
+    const int slot = in ? __ldg(slots + tok) : -1;
+    const int sh = __ffs(c.page) - 1;
+    const bool live = slot >= 0 && (slot >> sh) < c.pages;
+    float x[8];
+    const int64_t at = tok * (isv ? v_stride : k_stride) + rest * 8;
+    if (BF16) {
+        uint4 r = make_uint4(0u, 0u, 0u, 0u);
+        if (live) r = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(isv ? v : k) + at));
+        const uint32_t q[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[2 * j] = __uint_as_float(q[j] << 16);
+            x[2 * j + 1] = __uint_as_float(q[j] & 0xFFFF0000u);
+        }
+    } else {
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
+        if (live) {
+            const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(isv ? v : k) + at);
+            a = __ldcs(s);
+            b = __ldcs(s + 1);
+        }
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    if (!live) return;
+    const float step = kv4_step(m);
+    const int64_t cell = (static_cast<int64_t>(slot >> sh) * c.heads + head) * c.page + (slot & (c.page - 1));
+    reinterpret_cast<uint32_t*>(isv ? c.vc : c.kc)[cell * words + w] = kv4_pack8(x, step);
+    if ((w & 3) == 0)
+        (isv ? c.vs : c.ks)[cell * (words >> 2) + (w >> 2)] = static_cast<uint16_t>(__float_as_uint(step) >> 16);
+}
+
+// ------------------------------------------------------------------ gather
+// Two bf16 values code * step from nibbles at bits 3..6 and 19..22 of v: one logic op
+// flips the nibble's top bit and puts it under the exponent of 16 (16 + (code + 8)); one packed FMA
+// with (step, -24 * step) leaves code * step.  Exact for steps of at most 5 significant bits.
+__device__ __forceinline__ uint32_t kv4_pair(uint32_t v, uint32_t step2, uint32_t off2) {
+    uint32_t x, r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(x) : "r"(v), "r"(0x00780078u), "r"(0x41C041C0u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(step2), "r"(off2));
+    return r;
+}
+// -24 * step for a pair of steps (two products, one rounding each, exact for 5-bit steps).
+__device__ __forceinline__ uint32_t kv4_off(uint32_t step2) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(step2), "r"(0xC1C0C1C0u));
+    return r;
+}
+
+// Thread = 8 channels of one token and head: 4 bytes of codes in, 16 bytes out; rows without a slot
+// are zero.
+__global__ void __launch_bounds__(kKvBlock)
+kv4_gather_kernel(const Kv4View c, const int* __restrict__ slots, int64_t items, uint16_t* __restrict__ k,
+                  uint16_t* __restrict__ v) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * kKvBlock + threadIdx.x;
+    if (i >= 2 * items) return;
+    const bool isv = i >= items;
+    const int64_t u = isv ? i - items : i;
+    const int words = c.dim >> 3;
+    const int row = c.heads * words;
+    const int64_t tok = u / row;
+    const int rest = static_cast<int>(u - tok * row);
+    const int head = rest / words, w = rest - head * words;
+    const int slot = __ldg(slots + tok);
+    const int sh = __ffs(c.page) - 1;
+    uint4 o = make_uint4(0u, 0u, 0u, 0u);
+    if (slot >= 0 && (slot >> sh) < c.pages) {
+        const int64_t cell = (static_cast<int64_t>(slot >> sh) * c.heads + head) * c.page + (slot & (c.page - 1));
+        const uint32_t q = reinterpret_cast<const uint32_t*>(isv ? c.vc : c.kc)[cell * words + w];
+        const uint32_t s = (isv ? c.vs : c.ks)[cell * (words >> 2) + (w >> 2)];
+        const uint32_t s2 = s | (s << 16), o2 = kv4_off(s2);
+        const uint32_t a = kv4_pair(q << 3, s2, o2), b = kv4_pair(q >> 1, s2, o2);      // channels (0, 4), (1, 5)
+        const uint32_t e = kv4_pair(q >> 5, s2, o2), f = kv4_pair(q >> 9, s2, o2);      // (2, 6), (3, 7)
+        o = make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(e, f, 0x5410), __byte_perm(a, b, 0x7632),
+                       __byte_perm(e, f, 0x7632));
+    }
+    reinterpret_cast<uint4*>(isv ? v : k)[u] = o;
+}
+
+}  // namespace qat4

@@ -23,6 +23,8 @@
 #include "fq_gemm.cuh"
 #include "fq_staged.cuh"
 #include "refine.cuh"
+#include "kv4_cache.cuh"
+#include "kv4_attn.cuh"
 
 namespace {
 
@@ -44,6 +46,7 @@ struct DeviceInfo {
     int smem_optin = 0;       // opt-in shared memory per block; gemv attributes set when > 0
     bool fq_attr = false;
     bool gemm_attr = false;
+    bool kv4_attr = false;    // kv4_tables and kv4_attention kernels
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mutex;
@@ -840,6 +843,234 @@ qat4_status qat4_refine(const float* W, int64_t R, int64_t C, const float* H, in
 }
 
 // ------------------------------------------------------------ error handling
+}  // extern "C"
+
+// ------------------------------------------------------- 4-bit key/value cache
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static qat4_status kv4_cache_check(const qat4_kv4_cache* c) {
+    if (!c || !c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales) return QAT4_ERR_NULL;
+    const int32_t P = c->page_size, D = c->head_dim;
+    if ((P != 16 && P != 32 && P != 64 && P != 128) || (D != 64 && D != 128) || c->kv_heads < 1 || c->kv_heads > 1024 ||
+        c->num_pages < 1 || c->num_pages > (int64_t(1) << 31) - 1 || c->num_pages * P > (int64_t(1) << 31) - 1)
+        return QAT4_ERR_SHAPE;
+    if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) || !aligned16(c->v_scales))
+        return QAT4_ERR_ALIGN;
+    return QAT4_OK;
+}
+
+static qat4::Kv4View kv4_view(const qat4_kv4_cache* c) {
+    return {c->k_codes, c->k_scales, c->v_codes, c->v_scales, c->num_pages, c->page_size, c->kv_heads, c->head_dim};
+}
+
+// A launch that may overlap the end of the kernel before it in the stream (each of these kernels
+// waits for that kernel before it touches memory).
+template <typename... P, typename... A>
+static bool launch_pdl(void (*kernel)(P...), dim3 grid, int block, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(block));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
+template <typename K>
+static bool smem_attr(K kernel, size_t bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) == cudaSuccess;
+}
+
+template <int D, int ROWS>
+static bool kv4_decode_attr() {
+    return smem_attr(qat4::kv4_decode_kernel<D, ROWS>, qat4::KaLayout<D, ROWS>::kSmem);
+}
+
+// Shared-memory limits of the cache's kernels, once per context.
+static bool kv4_attrs(DeviceInfo* info) {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (info->kv4_attr) return true;
+    if (!smem_attr(qat4::kv4_tables_kernel, qat4::tables_smem_bytes(qat4::kTbMaxRequests))) return false;
+    if (!kv4_decode_attr<64, 8>() || !kv4_decode_attr<64, 16>() || !kv4_decode_attr<128, 8>() ||
+        !kv4_decode_attr<128, 16>())
+        return false;
+    info->kv4_attr = true;
+    return true;
+}
+
+static bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+    const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
+    return x < y + nb && y < x + na;
+}
+
+extern "C" {
+
+qat4_status qat4_kv4_tables(const int32_t* lengths, const int32_t* new_lengths, int64_t B, int32_t* block_table,
+                            int64_t table_stride, int64_t max_blocks, const int32_t* free_pages, int64_t num_free,
+                            int32_t page_size, int32_t* seq_lens, int32_t* cu_new, int32_t* slots,
+                            int64_t num_slots, int32_t* taken, cudaStream_t stream) {
+    if (!lengths || !new_lengths || !block_table || (!free_pages && num_free > 0) || !seq_lens || !cu_new ||
+        (!slots && num_slots > 0) || !taken)
+        return QAT4_ERR_NULL;
+    const int64_t top = (int64_t(1) << 31) - 1;
+    if (B < 1 || B > qat4::kTbMaxRequests || max_blocks < 1 || max_blocks > top || table_stride < max_blocks ||
+        table_stride > (int64_t(1) << 40) || num_free < 0 || num_free > top || num_slots < 0 || num_slots > top ||
+        (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128))
+        return QAT4_ERR_SHAPE;
+    for (const int32_t* in : {lengths, new_lengths}) {
+        if (overlap(in, 4 * B, seq_lens, 4 * B) || overlap(in, 4 * B, cu_new, 4 * (B + 1)) ||
+            overlap(in, 4 * B, slots, 4 * num_slots) || overlap(in, 4 * B, taken, 4) ||
+            overlap(in, 4 * B, block_table, 4 * ((B - 1) * table_stride + max_blocks)))
+            return QAT4_ERR_SHAPE;
+    }
+    for (const void* q : {static_cast<const void*>(lengths), static_cast<const void*>(new_lengths),
+                          static_cast<const void*>(block_table), static_cast<const void*>(free_pages),
+                          static_cast<const void*>(seq_lens), static_cast<const void*>(cu_new),
+                          static_cast<const void*>(slots), static_cast<const void*>(taken)})
+        if (!aligned4(q)) return QAT4_ERR_ALIGN;
+    int dev = 0;
+    DeviceInfo* info = nullptr;
+    if (!device_info(&dev, &info) || !kv4_attrs(info)) return QAT4_ERR_CUDA;
+    qat4::TablesParams p;
+    p.lengths = lengths;
+    p.fresh = new_lengths;
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.free_pages = free_pages;
+    p.seq_lens = seq_lens;
+    p.cu = cu_new;
+    p.slots = slots;
+    p.taken = taken;
+    p.num_slots = num_slots;
+    p.B = static_cast<int>(B);
+    p.max_blocks = static_cast<int>(max_blocks);
+    p.num_free = static_cast<int>(num_free);
+    p.page = page_size;
+    p.vec = aligned16(slots) ? 1 : 0;
+    // four tokens per thread, and a warp for every few requests
+    const int64_t want = std::max((num_slots + 4 * qat4::kTbThreads - 1) / (4 * qat4::kTbThreads), (B + 63) / 64);
+    const unsigned grid = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(want, info->sms)));
+    return launch_pdl(qat4::kv4_tables_kernel, dim3(grid), qat4::kTbThreads, qat4::tables_smem_bytes(p.B), stream, p)
+               ? QAT4_OK : QAT4_ERR_CUDA;
+}
+
+qat4_status qat4_kv4_append(const qat4_kv4_cache* cache, const void* k, const void* v, qat4_dtype dtype,
+                            int64_t k_stride, int64_t v_stride, const int32_t* slots, int64_t n,
+                            cudaStream_t stream) {
+    const qat4_status st = kv4_cache_check(cache);
+    if (st != QAT4_OK) return st;
+    if (n != 0 && (!k || !v || !slots)) return QAT4_ERR_NULL;
+    if (dtype != QAT4_F32 && dtype != QAT4_BF16) return QAT4_ERR_DTYPE;
+    const int64_t row = static_cast<int64_t>(cache->kv_heads) * cache->head_dim, top = int64_t(1) << 31;
+    const int64_t unit = dtype == QAT4_BF16 ? 8 : 4;      // elements in 16 bytes
+    if (n < 0 || n >= top || k_stride < row || v_stride < row || k_stride >= top || v_stride >= top ||
+        n * (row / 8) > (int64_t(1) << 37))
+        return QAT4_ERR_SHAPE;
+    if (k_stride % unit != 0 || v_stride % unit != 0 || !aligned16(k) || !aligned16(v) || !aligned4(slots))
+        return QAT4_ERR_ALIGN;
+    if (n == 0) return QAT4_OK;
+    const int64_t items = n * (row / 8);
+    const dim3 grid(static_cast<unsigned>((2 * items + qat4::kKvBlock - 1) / qat4::kKvBlock));
+    const qat4::Kv4View c = kv4_view(cache);
+    const bool ok = dtype == QAT4_BF16
+        ? launch_pdl(qat4::kv4_append_kernel<true>, grid, qat4::kKvBlock, 0, stream, c, k, v, k_stride, v_stride, slots, items)
+        : launch_pdl(qat4::kv4_append_kernel<false>, grid, qat4::kKvBlock, 0, stream, c, k, v, k_stride, v_stride, slots, items);
+    return ok ? QAT4_OK : QAT4_ERR_CUDA;
+}
+
+qat4_status qat4_kv4_gather(const qat4_kv4_cache* cache, const int32_t* slots, int64_t n, uint16_t* k, uint16_t* v,
+                            cudaStream_t stream) {
+    const qat4_status st = kv4_cache_check(cache);
+    if (st != QAT4_OK) return st;
+    if (n != 0 && (!k || !v || !slots)) return QAT4_ERR_NULL;
+    const int64_t row = static_cast<int64_t>(cache->kv_heads) * cache->head_dim;
+    if (n < 0 || n >= (int64_t(1) << 31) || n * (row / 8) > (int64_t(1) << 37)) return QAT4_ERR_SHAPE;
+    if (!aligned16(k) || !aligned16(v) || !aligned4(slots)) return QAT4_ERR_ALIGN;
+    if (n == 0) return QAT4_OK;
+    const int64_t items = n * (row / 8);
+    const dim3 grid(static_cast<unsigned>((2 * items + qat4::kKvBlock - 1) / qat4::kKvBlock));
+    return launch_pdl(qat4::kv4_gather_kernel, grid, qat4::kKvBlock, 0, stream, kv4_view(cache), slots, items, k, v)
+               ? QAT4_OK : QAT4_ERR_CUDA;
+}
+
+// Grid of the decode kernel: two CTAs per SM of a B200.  The same number on any device, so that the
+// workspace size does not depend on it; a device with fewer SMs runs the CTAs in waves.
+static constexpr int kKaGrid = 2 * 148;
+
+size_t qat4_kv4_attention_workspace_bytes(int64_t N, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+    if (N < 0 || B < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128))
+        return 0;
+    return static_cast<size_t>(kKaGrid) * 2 * (16 + 16 * (static_cast<size_t>(head_dim) + 2) * 4);
+}
+
+}  // extern "C"
+
+template <int D, int ROWS>
+static bool kv4_decode_launch(const qat4::AttnParams& p, cudaStream_t stream) {
+    return launch_pdl(qat4::kv4_decode_kernel<D, ROWS>, dim3(kKaGrid), qat4::kKaThreads, qat4::KaLayout<D, ROWS>::kSmem,
+                      stream, p) &&
+           launch_pdl(qat4::kv4_combine_kernel<D, ROWS>, dim3(kKaGrid, 4), qat4::kKcThreads, 0, stream, p, kKaGrid);
+}
+
+extern "C" {
+
+qat4_status qat4_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t N, int64_t q_heads,
+                               const qat4_kv4_cache* cache, const int32_t* block_table, int64_t table_stride,
+                               int64_t max_blocks, const int32_t* seq_lens, const int32_t* cu_q, int64_t B,
+                               float scale, int32_t causal, int32_t window, uint16_t* out, float* lse,
+                               void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    const qat4_status st = kv4_cache_check(cache);
+    if (st != QAT4_OK) return st;
+    if (!block_table || !seq_lens || !cu_q || (N != 0 && (!q || !out)) || !workspace) return QAT4_ERR_NULL;
+    const int64_t top = (int64_t(1) << 31) - 1, D = cache->head_dim, H = cache->kv_heads;
+    if (N < 0 || B < 1 || B > 65536 || q_heads < 1 || q_heads % H != 0 || q_heads / H > 64 || q_heads > 65536 ||
+        N > top / q_heads || q_stride < q_heads * D || q_stride > top || max_blocks < 1 || max_blocks > top ||
+        table_stride < max_blocks || table_stride > (int64_t(1) << 40) || !(scale > 0.0f) || !std::isfinite(scale) ||
+        !std::isfinite(scale * 1.4426950408889634f) || (causal != 0 && causal != 1) || window < 0 ||
+        (window > 0 && !causal))
+        return QAT4_ERR_SHAPE;
+    if (!aligned16(q) || q_stride % 8 != 0 || !aligned16(out) || !aligned16(workspace) || !aligned4(block_table) ||
+        !aligned4(seq_lens) || !aligned4(cu_q) || !aligned4(lse))
+        return QAT4_ERR_ALIGN;
+    if (workspace_bytes < qat4_kv4_attention_workspace_bytes(N, B, q_heads, H, D)) return QAT4_ERR_WORKSPACE;
+    if (N == 0) return QAT4_OK;
+    int dev = 0;
+    DeviceInfo* info = nullptr;
+    if (!device_info(&dev, &info) || !kv4_attrs(info)) return QAT4_ERR_CUDA;
+    qat4::AttnParams p;
+    p.q = q;
+    p.q_stride = q_stride;
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.seq_lens = seq_lens;
+    p.cu_q = cu_q;
+    p.out = out;
+    p.lse = lse;
+    p.meta = static_cast<int4*>(workspace);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + 2 * kKaGrid * sizeof(int4));
+    p.c = kv4_view(cache);
+    p.N = static_cast<int>(N);
+    p.B = static_cast<int>(B);
+    p.Hq = static_cast<int>(q_heads);
+    p.group = static_cast<int>(q_heads / H);
+    p.max_blocks = static_cast<int>(max_blocks);
+    p.causal = causal;
+    p.window = window;
+    p.rows_lo = 1;
+    p.rows_hi = 0x7fffffff;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    // generous bound of a wait: 10 s (a CTA waits for one unit's copies, some microseconds)
+    p.limit_ns = 10000000000ull;
+    const bool half = N * p.group <= 8 * B;      // tiles of 8 rows where the average request has no more
+    const bool ok = D == 64 ? (half ? kv4_decode_launch<64, 8>(p, stream) : kv4_decode_launch<64, 16>(p, stream))
+                            : (half ? kv4_decode_launch<128, 8>(p, stream) : kv4_decode_launch<128, 16>(p, stream));
+    return ok ? QAT4_OK : QAT4_ERR_CUDA;
+}
+
 qat4_status qat4_sync_check(cudaStream_t stream) {
     if (cudaStreamSynchronize(stream) != cudaSuccess) return QAT4_ERR_CUDA;
     int word = 0;
