@@ -516,43 +516,54 @@ def kv4_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, devi
                       for _ in range(2) for s, d in ((codes, torch.uint8), (scales, torch.bfloat16))))
 
 
+def _arg(t, name, dtype, shape=None):
+    """Pointer of a contiguous CUDA tensor; what _dev refuses is refused by _dev (these calls take a few
+    microseconds on the device, so the accepting path is kept short)."""
+    if t.is_cuda and t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, name, dtype, shape)
+
+
 def _cache_struct(cache):
     import torch
-    kc = cache[0]
+    kc, ks, vc, vs = cache
     if not isinstance(kc, torch.Tensor) or kc.dim() != 4:
         raise ValueError("k_codes must be [num_pages, kv_heads, page_size, head_dim / 2]")
-    n, h, p, half = kc.shape
-    scales = (n, h, p, half // 16)
-    return _CacheStruct(_dev(kc, "k_codes", torch.uint8), _dev(cache[1], "k_scales", torch.bfloat16, scales),
-                        _dev(cache[2], "v_codes", torch.uint8, kc.shape), _dev(cache[3], "v_scales", torch.bfloat16, scales),
+    n, h, p, half = codes = kc.shape
+    steps = (n, h, p, half // 16)
+    return _CacheStruct(_arg(kc, "k_codes", torch.uint8), _arg(ks, "k_scales", torch.bfloat16, steps),
+                        _arg(vc, "v_codes", torch.uint8, codes), _arg(vs, "v_scales", torch.bfloat16, steps),
                         n, p, h, 2 * half)
 
 
 def _same_device(first, *others):
-    """The CUDA device that all tensors must share; the call is made with it current."""
+    """Index of the CUDA device that all tensors share; the call is made with it current."""
+    d = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != d:
             raise ValueError(f"all tensors must be on one device, got {first.device} and {t.device}")
-    return first.device
+    return d
 
 
 class _on:
-    """Makes the tensors' device current for a call, and `stream` (when given) the current stream, so that
-    outputs and workspaces allocated inside belong to the stream that uses them."""
+    """Makes device `d` current for a call, and `stream` (when given) the current stream, so that outputs and
+    workspaces allocated inside belong to the stream that uses them; gives the stream's handle."""
+    __slots__ = ("d", "stream", "guards")
 
-    def __init__(self, device, stream):
-        import torch
-        self.guards = []
-        if device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-            self.guards.append(torch.cuda.stream(stream))
+    def __init__(self, d, stream):
+        self.d, self.stream, self.guards = d, stream, ()
 
     def __enter__(self):
+        import torch
+        s = self.stream
+        if s is None and torch._C._cuda_getDevice() == self.d:
+            return torch._C._cuda_getCurrentRawStream(self.d)
+        if s is not None and s.device.index != self.d:
+            raise ValueError(f"the stream is on {s.device}, the tensors on cuda:{self.d}")
+        self.guards = (torch.cuda.device(self.d),) if s is None else (torch.cuda.device(self.d), torch.cuda.stream(s))
         for g in self.guards:
             g.__enter__()
+        return torch.cuda.current_stream(self.d).cuda_stream
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
@@ -594,27 +605,27 @@ def kv4_tables(lengths, new_lengths, block_table, free_pages, page_size, num_slo
     was too short: the tokens without a page have slot -1."""
     import torch
     L = lib()
-    lp = _dev(lengths, "lengths", torch.int32)
+    lp = _arg(lengths, "lengths", torch.int32)
     if lengths.dim() != 1 or lengths.shape[0] < 1:
         raise ValueError("lengths must be [B] with B >= 1")
     B = lengths.shape[0]
-    np_ = _dev(new_lengths, "new_lengths", torch.int32, (B,))
+    np_ = _arg(new_lengths, "new_lengths", torch.int32, (B,))
     tp, ts = _table(block_table)
     if block_table.shape[0] != B:
         raise ValueError(f"block_table must have {B} rows, got {block_table.shape[0]}")
-    fp = _dev(free_pages, "free_pages", torch.int32)
+    fp = _arg(free_pages, "free_pages", torch.int32)
     dev = _same_device(lengths, new_lengths, block_table, free_pages, seq_lens, cu_new, slots, taken)
     num_slots, page_size = int(num_slots), int(page_size)
     if num_slots < 0 or num_slots >= 1 << 31 or page_size not in (16, 32, 64, 128):
         raise ValueError("num_slots must be in [0, 2^31), page_size 16, 32, 64 or 128")
-    with _on(dev, stream):
+    with _on(dev, stream) as handle:
         seq_lens = _out(seq_lens, "seq_lens", (B,), torch.int32, lengths)
         cu_new = _out(cu_new, "cu_new", (B + 1,), torch.int32, lengths)
         slots = _out(slots, "slots", (num_slots,), torch.int32, lengths)
         taken = _out(taken, "taken", (), torch.int32, lengths)
         _check(L.qat4_kv4_tables(lp, np_, B, tp, ts, block_table.shape[1], fp, free_pages.numel(), page_size,
                                  seq_lens.data_ptr(), cu_new.data_ptr(), slots.data_ptr(), num_slots,
-                                 taken.data_ptr(), _stream(stream)), "qat4_kv4_tables")
+                                 taken.data_ptr(), handle), "qat4_kv4_tables")
     return seq_lens, cu_new, slots, taken
 
 
@@ -629,9 +640,9 @@ def kv4_append(cache, k, v, slots, stream=None):
     vp, vs = _rows3(v, "v", c.kv_heads, c.head_dim, (k.dtype,))
     if v.shape[0] != k.shape[0]:
         raise ValueError("k and v must have the same number of tokens")
-    sp = _dev(slots, "slots", torch.int32, (k.shape[0],))
-    with _on(_same_device(k, v, slots, *cache), stream):
-        _check(L.qat4_kv4_append(ct.byref(c), kp, vp, _gdtype(k), ks, vs, sp, k.shape[0], _stream(stream)),
+    sp = _arg(slots, "slots", torch.int32, (k.shape[0],))
+    with _on(_same_device(k, v, slots, *cache), stream) as handle:
+        _check(L.qat4_kv4_append(ct.byref(c), kp, vp, _gdtype(k), ks, vs, sp, k.shape[0], handle),
                "qat4_kv4_append")
 
 
@@ -641,14 +652,14 @@ def kv4_gather(cache, slots, k=None, v=None, stream=None):
     import torch
     L = lib()
     c = _cache_struct(cache)
-    sp = _dev(slots, "slots", torch.int32)
+    sp = _arg(slots, "slots", torch.int32)
     if slots.dim() != 1:
         raise ValueError("slots must be [n]")
     shape = (slots.shape[0], c.kv_heads, c.head_dim)
-    with _on(_same_device(slots, k, v, *cache), stream):
+    with _on(_same_device(slots, k, v, *cache), stream) as handle:
         k = _out(k, "k", shape, torch.bfloat16, slots)
         v = _out(v, "v", shape, torch.bfloat16, slots)
-        _check(L.qat4_kv4_gather(ct.byref(c), sp, shape[0], k.data_ptr(), v.data_ptr(), _stream(stream)),
+        _check(L.qat4_kv4_gather(ct.byref(c), sp, shape[0], k.data_ptr(), v.data_ptr(), handle),
                "qat4_kv4_gather")
     return k, v
 
@@ -676,20 +687,20 @@ def kv4_attention(q, cache, block_table, seq_lens, cu_q, scale=None, causal=True
     qp, qs = _rows3(q, "q", Hq, c.head_dim, (torch.bfloat16,))
     tp, ts = _table(block_table)
     B = block_table.shape[0]
-    lp = _dev(seq_lens, "seq_lens", torch.int32, (B,))
-    cp = _dev(cu_q, "cu_q", torch.int32, (B + 1,))
+    lp = _arg(seq_lens, "seq_lens", torch.int32, (B,))
+    cp = _arg(cu_q, "cu_q", torch.int32, (B + 1,))
     dev = _same_device(q, block_table, seq_lens, cu_q, out, lse, workspace, *cache)
     scale = 1.0 / math.sqrt(c.head_dim) if scale is None else float(scale)
     window = max(-1, min(int(window), 0x7fffffff))
-    with _on(dev, stream):
+    with _on(dev, stream) as handle:
         out = _out(out, "out", (N, Hq, c.head_dim), torch.bfloat16, q)
-        need = int(L.qat4_kv4_attention_workspace_bytes(N, B, Hq, c.kv_heads, c.head_dim))
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            need = L.qat4_kv4_attention_workspace_bytes(N, B, Hq, c.kv_heads, c.head_dim)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         _check(L.qat4_kv4_attention(qp, qs, N, Hq, ct.byref(c), tp, ts, block_table.shape[1], lp, cp, B, scale,
                                     int(bool(causal)), window, out.data_ptr(),
-                                    _dev(lse, "lse", torch.float32, (N, Hq)) if lse is not None else None,
-                                    _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream)),
+                                    _arg(lse, "lse", torch.float32, (N, Hq)) if lse is not None else None,
+                                    _arg(workspace, "workspace", torch.uint8), workspace.numel(), handle),
                "qat4_kv4_attention")
     return out
 

@@ -25,6 +25,7 @@
 #include "refine.cuh"
 #include "kv4_cache.cuh"
 #include "kv4_attn.cuh"
+#include "kv4_prefill.cuh"
 
 namespace {
 
@@ -890,6 +891,16 @@ static bool kv4_decode_attr() {
     return smem_attr(qat4::kv4_decode_kernel<D, ROWS>, qat4::KaLayout<D, ROWS>::kSmem);
 }
 
+// The prefill kernel's warpgroups trade registers: their shares must fit what the block is launched with, or
+// the growing ones would wait for good.
+template <int D>
+static bool kv4_prefill_attr() {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, qat4::kv4_prefill_kernel<D>) == cudaSuccess &&
+           at.numRegs * qat4::kKpThreads >= 128 * (2 * qat4::kKpRegsSoftmax + qat4::kKpRegsDecode + qat4::kKpRegsIssue) &&
+           smem_attr(qat4::kv4_prefill_kernel<D>, qat4::KpLayout<D>::kSmem);
+}
+
 // Shared-memory limits of the cache's kernels, once per context.
 static bool kv4_attrs(DeviceInfo* info) {
     std::lock_guard<std::mutex> lock(g_mutex);
@@ -898,6 +909,7 @@ static bool kv4_attrs(DeviceInfo* info) {
     if (!kv4_decode_attr<64, 8>() || !kv4_decode_attr<64, 16>() || !kv4_decode_attr<128, 8>() ||
         !kv4_decode_attr<128, 16>())
         return false;
+    if (!kv4_prefill_attr<64>() || !kv4_prefill_attr<128>()) return false;
     info->kv4_attr = true;
     return true;
 }
@@ -997,23 +1009,71 @@ qat4_status qat4_kv4_gather(const qat4_kv4_cache* cache, const int32_t* slots, i
                ? QAT4_OK : QAT4_ERR_CUDA;
 }
 
-// Grid of the decode kernel: two CTAs per SM of a B200.  The same number on any device, so that the
-// workspace size does not depend on it; a device with fewer SMs runs the CTAs in waves.
-static constexpr int kKaGrid = 2 * 148;
+}  // extern "C"
 
-size_t qat4_kv4_attention_workspace_bytes(int64_t N, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
-    if (N < 0 || B < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128))
-        return 0;
-    return static_cast<size_t>(kKaGrid) * 2 * (16 + 16 * (static_cast<size_t>(head_dim) + 2) * 4);
+// Grid of the decode kernel: two CTAs per SM of a B200, and SMs for the split of the prefill kernel.  The same
+// numbers on any device, so that the workspace size does not depend on it; a device with fewer SMs runs the
+// CTAs in waves.
+static constexpr int kKaSms = 148;
+static constexpr int kKaGrid = 2 * kKaSms;
+
+// Which kernels serve a call, from what the host knows of it: N query tokens of B requests.
+//   average rows per request and kv head <= 32: the decode kernel takes every request (decode steps, drafts);
+//   more, and one request: the prefill kernel takes it;
+//   more, and several: requests of up to kRowsDecode rows go to the decode kernel, the others to the prefill
+//   kernel.
+struct Kv4Plan {
+    bool decode, prefill;
+    int lo_decode, hi_decode, lo_prefill;
+    int64_t tiles;        // upper bound of the prefill kernel's row tiles
+    int splits;           // most parts that the keys of a row tile are cut into
+};
+static constexpr int kRowsDecode = 64;
+
+static Kv4Plan kv4_plan(int64_t N, int64_t B, int64_t group, int64_t kv_heads) {
+    Kv4Plan pl = {true, false, 1, 0x7fffffff, 1, 0, 1};
+    const int64_t rows = N * group;
+    if (rows <= 32 * B) return pl;
+    pl.prefill = true;
+    pl.decode = B > 1;
+    if (pl.decode) {
+        pl.hi_decode = kRowsDecode;
+        pl.lo_prefill = kRowsDecode + 1;
+    }
+    pl.tiles = rows / qat4::kKpRows + std::min(B, rows / pl.lo_prefill);
+    pl.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, kKaSms / (pl.tiles * kv_heads))));
+    return pl;
 }
 
-}  // extern "C"
+static size_t kv4_decode_bytes(int64_t D) {
+    return static_cast<size_t>(kKaGrid) * 2 * (16 + 16 * (static_cast<size_t>(D) + 2) * 4);
+}
+
+extern "C" size_t qat4_kv4_attention_workspace_bytes(int64_t N, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+    if (N < 0 || B < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128) ||
+        N > ((int64_t(1) << 31) - 1) / q_heads)
+        return 0;
+    const Kv4Plan pl = kv4_plan(N, B, q_heads / kv_heads, kv_heads);
+    size_t bytes = kv4_decode_bytes(head_dim);
+    if (pl.splits > 1)
+        bytes += (static_cast<size_t>(pl.splits) * N * q_heads * (head_dim + 2) * 4 + 255) & ~size_t(255);
+    return bytes;
+}
 
 template <int D, int ROWS>
 static bool kv4_decode_launch(const qat4::AttnParams& p, cudaStream_t stream) {
     return launch_pdl(qat4::kv4_decode_kernel<D, ROWS>, dim3(kKaGrid), qat4::kKaThreads, qat4::KaLayout<D, ROWS>::kSmem,
                       stream, p) &&
            launch_pdl(qat4::kv4_combine_kernel<D, ROWS>, dim3(kKaGrid, 4), qat4::kKcThreads, 0, stream, p, kKaGrid);
+}
+
+template <int D>
+static bool kv4_prefill_launch(const qat4::PrefillParams& p, int64_t tiles, cudaStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(tiles * p.a.c.heads), static_cast<unsigned>(p.splits));
+    if (!launch_pdl(qat4::kv4_prefill_kernel<D>, grid, qat4::kKpThreads, qat4::KpLayout<D>::kSmem, stream, p)) return false;
+    if (p.splits == 1) return true;
+    const int64_t rows = static_cast<int64_t>(p.a.N) * p.a.Hq;
+    return launch_pdl(qat4::kv4_join_kernel<D>, dim3(static_cast<unsigned>((rows + 7) / 8)), qat4::kKjThreads, 0, stream, p);
 }
 
 extern "C" {
@@ -1028,7 +1088,7 @@ qat4_status qat4_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t N, i
     if (!block_table || !seq_lens || !cu_q || (N != 0 && (!q || !out)) || !workspace) return QAT4_ERR_NULL;
     const int64_t top = (int64_t(1) << 31) - 1, D = cache->head_dim, H = cache->kv_heads;
     if (N < 0 || B < 1 || B > 65536 || q_heads < 1 || q_heads % H != 0 || q_heads / H > 64 || q_heads > 65536 ||
-        N > top / q_heads || q_stride < q_heads * D || q_stride > top || max_blocks < 1 || max_blocks > top ||
+        N > top / q_heads || N * q_heads / H / qat4::kKpRows + B > top / (16 * H) || q_stride < q_heads * D || q_stride > top || max_blocks < 1 || max_blocks > top ||
         table_stride < max_blocks || table_stride > (int64_t(1) << 40) || !(scale > 0.0f) || !std::isfinite(scale) ||
         !std::isfinite(scale * 1.4426950408889634f) || (causal != 0 && causal != 1) || window < 0 ||
         (window > 0 && !causal))
@@ -1060,14 +1120,29 @@ qat4_status qat4_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t N, i
     p.max_blocks = static_cast<int>(max_blocks);
     p.causal = causal;
     p.window = window;
-    p.rows_lo = 1;
-    p.rows_hi = 0x7fffffff;
     p.scale_log2 = scale * 1.4426950408889634f;
-    // generous bound of a wait: 10 s (a CTA waits for one unit's copies, some microseconds)
+    // generous bound of a wait: 10 s (a CTA waits for one unit's copies or one block's products, microseconds)
     p.limit_ns = 10000000000ull;
-    const bool half = N * p.group <= 8 * B;      // tiles of 8 rows where the average request has no more
-    const bool ok = D == 64 ? (half ? kv4_decode_launch<64, 8>(p, stream) : kv4_decode_launch<64, 16>(p, stream))
-                            : (half ? kv4_decode_launch<128, 8>(p, stream) : kv4_decode_launch<128, 16>(p, stream));
+    const Kv4Plan pl = kv4_plan(N, B, p.group, H);
+    bool ok = true;
+    if (pl.decode) {
+        p.rows_lo = pl.lo_decode;
+        p.rows_hi = pl.hi_decode;
+        const bool half = N * p.group <= 8 * B;      // tiles of 8 rows where the average request has no more
+        ok = D == 64 ? (half ? kv4_decode_launch<64, 8>(p, stream) : kv4_decode_launch<64, 16>(p, stream))
+                     : (half ? kv4_decode_launch<128, 8>(p, stream) : kv4_decode_launch<128, 16>(p, stream));
+    }
+    if (ok && pl.prefill) {
+        qat4::PrefillParams pp;
+        p.rows_lo = pl.lo_prefill;
+        p.rows_hi = 0x7fffffff;
+        pp.a = p;
+        pp.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kv4_decode_bytes(D));
+        // a part holds at least four blocks of keys of the longest request that the table can name
+        pp.splits = static_cast<int>(std::max<int64_t>(
+            1, std::min<int64_t>(pl.splits, max_blocks * cache->page_size / (4 * qat4::kKpBlock))));
+        ok = D == 64 ? kv4_prefill_launch<64>(pp, pl.tiles, stream) : kv4_prefill_launch<128>(pp, pl.tiles, stream);
+    }
     return ok ? QAT4_OK : QAT4_ERR_CUDA;
 }
 
