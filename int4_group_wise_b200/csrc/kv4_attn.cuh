@@ -6,25 +6,28 @@
 //
 // Rows.  The group = q_heads / kv_heads query heads that share a key/value head
 // are packed with the request's query tokens into rows (token * group + head),
-// so a cached token is read once for all of them: a tile is ROWS = 8 or 16 rows
-// of the 16 of an mma.sync m16n8k16 (with 8, the accumulators and exponentials
-// of the upper half are left out).
+// so a cached token is read and decoded once for all rows of a tile (4, 8 or
+// 16).
 //
 // Bound: HBM.  A cached token of a head costs 2 * (D/2 + D/16) bytes (144 at
 // D = 128) and 4 * D * rows flop, far below the tensor cores' balance, so the
-// contractions run on mma.sync only to keep the issue slots for the decoding:
-// per pair of codes one shift, one logic op and one packed FMA (kv4_pair).  The
-// operand orders are chosen so that the packed words need no reordering:
-//   S = Q K^T: B = keys.  Thread (g, t) holds token g of an 8-token tile and its
-//     channels [32t, 32t + 32) (D = 128): 16 bytes of codes and one step; the
-//     8 MMAs of a tile take word w's pairs (0,4)(1,5) and (2,6)(3,7), and q is
-//     loaded once in that order.
-//   O = P V: B = values.  Thread (g, t) holds channels [16g, 16g + 16) of the
-//     tokens (2t, 2t+1), (2t+8, 2t+9); a byte permute pairs two tokens' words
-//     and the same decode gives the (token, token + 1) pairs of each channel.
-//     The accumulator columns of thread t are then 32 consecutive channels.
-// P is the accumulator of S rounded to bf16 (half a step, 2^-9 of each weight;
-// the row sum adds the unrounded weights), the statistics are float32.
+// contractions run on mma.sync (m16n8k16) only to keep the issue slots for the
+// decoding: per pair of codes one shift, one logic op and one packed FMA
+// (kv4_pair).  The rows are the MMA's narrow side, and the operand orders are
+// chosen so that the packed words need no reordering:
+//   S^T = K Q^T: A = 16 tokens.  Thread (g, t) holds tokens g and g + 8 and their
+//     channels [32t, 32t + 32) (D = 128): 16 bytes of codes and one step each;
+//     word w's pairs (0,4)(1,5) and (2,6)(3,7) are two MMAs, and q is loaded
+//     once in that order.
+//   O^T = V^T P^T: A = 16 channels x 16 tokens.  Thread (g, t) holds channels
+//     [16g, 16g + 16) of the tokens (2t, 2t+1), (2t+8, 2t+9); a byte permute
+//     pairs two tokens' words and the same decode gives the (token, token + 1)
+//     pairs of each channel.  P comes from S's accumulators by movmatrix, and
+//     a thread's outputs are 16 consecutive channels of two rows.
+// P is rounded to bf16 (at most 2^-8 of each weight; the row sum adds the
+// unrounded weights); a tile of 4 rows uses the other 4 columns of the MMA for
+// what that rounding left, so its weights enter with 16 bits.  Scores,
+// statistics and outputs are float32.
 //
 // Work split.  A unit is (request, kv head, row tile, chunk of 128 tokens); the
 // units of the whole ragged batch form one list (from the lengths, on the
@@ -54,7 +57,6 @@ namespace qat4 {
 constexpr int kKaWarps = 4;                       // consumer warps
 constexpr int kKaThreads = 32 * (kKaWarps + 1);   // + one producer warp
 constexpr int kKaChunk = 128;                     // tokens per unit
-constexpr int kKaStages = 4;
 constexpr float kKaGrow = 8.0f;   // a row's reference maximum moves only when exceeded by 2^8
 
 struct AttnParams {
@@ -111,14 +113,47 @@ __device__ __forceinline__ Units<ROWS> kv4_units(const AttnParams& p, const Requ
     return u;
 }
 
+// A place in the unit list: request b, kv head, row tile and chunk.
+template <int ROWS>
+struct Place {
+    Request r;
+    Units<ROWS> un;
+    int b, kvh, tile, ch;
+    __device__ __forceinline__ void start(const AttnParams& p, int b_, int64_t skip) {
+        b = b_;
+        r = kv4_request(p, b);
+        un = kv4_units<ROWS>(p, r);
+        ch = static_cast<int>(skip % un.chunks);
+        tile = static_cast<int>((skip / un.chunks) % un.tiles);
+        kvh = static_cast<int>(skip / (static_cast<int64_t>(un.chunks) * un.tiles));
+    }
+    // the next unit; `more`: there is one
+    __device__ __forceinline__ void next(const AttnParams& p, bool more) {
+        if (++ch < un.chunks) return;
+        ch = 0;
+        if (++tile < un.tiles) return;
+        tile = 0;
+        if (++kvh < p.c.heads || !more) return;
+        kvh = 0;
+        do {
+            ++b;
+            r = kv4_request(p, b);
+            un = kv4_units<ROWS>(p, r);
+        } while (un.tiles == 0);
+    }
+    __device__ __forceinline__ int t0() const { return (un.c0 + ch) * kKaChunk; }
+};
+
 template <int D, int ROWS>
 struct KaLayout {
     static constexpr int kCodes = kKaChunk * D / 2;
     static constexpr int kSteps = kKaChunk * (D / 32) * 2;
     static constexpr int kStage = 2 * kCodes + 2 * kSteps;
+    static constexpr int kStages = 4;                             // 73 KB of ring at D = 128
     static constexpr int kORow = D * 4 + 16;                      // bytes of an output row in the join buffer
     static constexpr int kJoin = kKaWarps * ROWS * kORow;
-    static constexpr size_t kSmem = static_cast<size_t>(kKaStages) * kStage + kJoin;
+    static constexpr int kPerSm = ROWS == 16 || D == 128 ? 2 : 3; // CTAs per SM (registers, shared memory)
+    static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStage + kJoin;
 };
 
 // Workspace floats of one piece: ROWS rows of D outputs, then ROWS maxima (log2) and ROWS sums.
@@ -152,19 +187,51 @@ __device__ __forceinline__ int64_t ka_out_row(const AttnParams& p, const Request
     return static_cast<int64_t>(r.q0 + tok) * p.Hq + kvh * p.group + (row - tok * p.group);
 }
 
-template <int D, int ROWS>
-__global__ void __launch_bounds__(kKaThreads, 2)
+// gm_mma with a zero accumulator.
+__device__ __forceinline__ void ka_mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+// Transposes an 8 x 8 matrix of 16-bit values held as one row pair per lane.
+__device__ __forceinline__ uint32_t ka_trans(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t a) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+    return v;
+}
+
+// CL: a cluster of kKaCluster CTAs per row tile, its chunks cut evenly and the pieces joined through
+// the cluster's shared memory: one launch and no workspace, for batches too small to fill the GPU.
+// Otherwise the stream of all units is cut evenly over the grid.
+constexpr int kKaCluster = 8;
+
+template <int D, int ROWS, bool CL>
+__global__ void __launch_bounds__(kKaThreads, KaLayout<D, ROWS>::kPerSm)
 kv4_decode_kernel(const AttnParams p) {
     using L = KaLayout<D, ROWS>;
-    constexpr bool kFull = ROWS == 16;
-    constexpr int kSteps = D / 16;             // MMAs along the channels of S
+    constexpr int kStages = L::kStages;
+    constexpr bool kLo = ROWS == 4;            // columns 4..7 carry the weights' rounding remainders
+    constexpr int kN = ROWS == 16 ? 2 : 1;     // MMA column tiles of 8 rows
     constexpr int kW = D / 32;                 // words of a thread's key channels (4 or 2)
     constexpr int kVW = D / 64;                // words of a thread's value channels (2 or 1)
-    constexpr int kNT = D / 8;                 // output tiles of 8 channels
+    constexpr int kM = D / 16;                 // output tiles of 16 channels
     extern __shared__ __align__(128) uint8_t ka_smem[];
-    __shared__ __align__(8) uint64_t full_bar[kKaStages], empty_bar[kKaStages];
-    __shared__ uint32_t live_bits[kKaStages][4];
+    __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
+    __shared__ uint32_t live_bits[kStages][4];
     __shared__ float join_m[kKaWarps][16], join_l[kKaWarps][16];
+    __shared__ __align__(16) float res[CL ? ka_piece<D, ROWS>() : 4];
     __shared__ int64_t scan[32], s_skip;
     __shared__ int s_b;
     __shared__ int abort_flag;
@@ -173,15 +240,15 @@ kv4_decode_kernel(const AttnParams p) {
     pdl_launch_dependents();
     pdl_wait();
 
-    // ---- this CTA's range of the unit list
+    // ---- this CTA's range of the unit list (of the tile list, in clusters)
+    auto count = [&](int b) -> int64_t {
+        const Units<ROWS> u = kv4_units<ROWS>(p, kv4_request(p, b));
+        return static_cast<int64_t>(u.tiles) * (CL ? 1 : u.chunks) * p.c.heads;
+    };
     const int per = (p.B + kKaThreads - 1) / kKaThreads;
     const int rb0 = min(p.B, tid * per), rb1 = min(p.B, rb0 + per);
     int64_t mine = 0;
-    for (int b = rb0; b < rb1; ++b) {
-        const Request r = kv4_request(p, b);
-        const Units<ROWS> u = kv4_units<ROWS>(p, r);
-        mine += static_cast<int64_t>(u.tiles) * u.chunks * p.c.heads;
-    }
+    for (int b = rb0; b < rb1; ++b) mine += count(b);
     int64_t incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -190,29 +257,34 @@ kv4_decode_kernel(const AttnParams p) {
     }
     if (lane == 31) scan[warp] = incl;
     if (tid == 0) {
-        s_b = p.B;
+        s_b = -1;
         abort_flag = 0;
-        for (int s = 0; s < kKaStages; ++s) {
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(&full_bar[s], 1);
             mbar_init(&empty_bar[s], kKaWarps);
         }
         fence_mbar_init();
     }
+    if (!CL && tid < 2) p.meta[2 * blockIdx.x + tid] = make_int4(-1, 0, 0, 0);
     __syncthreads();
     int64_t before = incl - mine, total = 0;
     for (int w = 0; w <= kKaWarps; ++w) {
         if (w < warp) before += scan[w];
         total += scan[w];
     }
-    const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);     // every CTA of these has work
-    const int64_t u0 = ctas > 0 && blockIdx.x < ctas ? total * blockIdx.x / ctas : 0;
-    const int64_t u1 = ctas > 0 && blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : 0;
+    int64_t u0, u1;
+    if (CL) {
+        u0 = blockIdx.x / kKaCluster;
+        u1 = u0 < total ? u0 + 1 : u0;
+    } else {
+        const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);     // every CTA of these has work
+        u0 = blockIdx.x < ctas ? total * blockIdx.x / ctas : 0;
+        u1 = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : 0;
+    }
     if (u0 < u1 && u0 >= before && u0 < before + mine) {
         int64_t at = before;
         for (int b = rb0; b < rb1; ++b) {
-            const Request r = kv4_request(p, b);
-            const Units<ROWS> u = kv4_units<ROWS>(p, r);
-            const int64_t n = static_cast<int64_t>(u.tiles) * u.chunks * p.c.heads;
+            const int64_t n = count(b);
             if (u0 < at + n) {
                 s_b = b;
                 s_skip = u0 - at;
@@ -222,22 +294,23 @@ kv4_decode_kernel(const AttnParams p) {
         }
     }
     __syncthreads();
-    int4* const meta = p.meta + 2 * blockIdx.x;
-    if (tid < 2) meta[tid] = make_int4(-1, 0, 0, 0);
-    if (u0 >= u1) return;
-    __syncthreads();                            // the records below overwrite these
+    if (u0 >= u1) return;                       // in clusters: every CTA of it
     volatile int* abort = &abort_flag;
-    const int b_first = s_b;
-    const int64_t skip = s_skip;
     const uint32_t ring = smem_u32(ka_smem);
-
-    // position in the list: request b, kv head, tile and chunk of unit u0
-    Request r = kv4_request(p, b_first);
-    Units<ROWS> un = kv4_units<ROWS>(p, r);
-    int b = b_first;
-    int ch = static_cast<int>(skip % un.chunks);
-    int tile = static_cast<int>((skip / un.chunks) % un.tiles);
-    int kvh = static_cast<int>(skip / (static_cast<int64_t>(un.chunks) * un.tiles));
+    Place<ROWS> at;
+    if (CL) {
+        const int rank = static_cast<int>(cluster_ctarank());
+        at.b = s_b;
+        at.r = kv4_request(p, at.b);
+        at.un = kv4_units<ROWS>(p, at.r);
+        at.kvh = static_cast<int>(s_skip / at.un.tiles);
+        at.tile = static_cast<int>(s_skip % at.un.tiles);
+        at.ch = at.un.chunks * rank / kKaCluster;
+        u0 = 0;
+        u1 = at.un.chunks * (rank + 1) / kKaCluster - at.ch;      // none for some ranks of a short request
+    } else {
+        at.start(p, s_b, s_skip);
+    }
     const int page = p.c.page, sh = __ffs(page) - 1;
 
     if (warp == kKaWarps) {
@@ -250,33 +323,39 @@ kv4_decode_kernel(const AttnParams p) {
                             : arr == 2 ? p.c.vc : reinterpret_cast<const uint8_t*>(p.c.vs);
         const uint32_t dst0 = (arr == 0 ? 0 : arr == 1 ? 2 * L::kCodes : arr == 2 ? L::kCodes : 2 * L::kCodes + L::kSteps) +
                               pi * page * unit;
+        // this lane's entry of the block table for a unit, -1 where nothing is to be copied; loaded one unit
+        // ahead, so that its latency is not part of the ring's round trip
+        auto entry = [&](const Place<ROWS>& x) -> int {
+            const int pt = x.t0() + pi * page;                 // first token of this lane's page
+            // pt < len keeps the index inside the table's row
+            return has && pt < x.r.len && pt + page > x.r.lo ? __ldg(p.table + x.b * p.table_stride + (pt >> sh)) : -1;
+        };
         int64_t issued = 0;
         int s = 0;
         uint32_t ph = 0;
+        int id = u0 < u1 ? entry(at) : -1;
         for (int64_t u = u0; u < u1; ++u) {
+            Place<ROWS> ahead = at;
+            ahead.next(p, u + 1 < u1);
+            const int id_next = u + 1 < u1 ? entry(ahead) : -1;
             int ok = 1;
             if (lane == 0) ok = mbar_wait(&empty_bar[s], ph ^ 1u, abort, p.limit_ns) ? 1 : 0;
             if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-            const int t0 = (un.c0 + ch) * kKaChunk;            // first token of the chunk
-            const int pt = t0 + pi * page;                     // first token of this lane's page
-            int id = -1;
-            if (has && pt < r.len && pt + page > r.lo) {       // pt < len keeps the index inside the table's row
-                id = __ldg(p.table + b * p.table_stride + (pt >> sh));
-                if (id < 0 || id >= p.c.pages) id = -1;
-            }
-            // tokens that exist, 32 per word: lanes 0..3 take one word each from the pages' votes
-            const uint32_t ids = __ballot_sync(0xffffffffu, has && arr == 0 && id >= 0);
+            if (id >= p.c.pages) id = -1;
+            const int t0 = at.t0(), pt = t0 + pi * page;
+            // tokens that exist, 32 per word in lanes 0..3: inside [lo, len) and of a page that exists
+            const uint32_t ids = __ballot_sync(0xffffffffu, arr == 0 && id >= 0);
             if (lane < 4) {
-                uint32_t m = 0;
-#pragma unroll 8
-                for (int j = 0; j < 32; ++j) {
-                    const int t = t0 + 32 * lane + j;
-                    if (t < r.len && t >= r.lo && ((ids >> ((t - t0) >> sh)) & 1u)) m |= 1u << j;
-                }
+                const int w0 = t0 + 32 * lane;
+                const int e = min(max(at.r.len - w0, 0), 32), f = min(max(at.r.lo - w0, 0), 32);
+                uint32_t m = (e == 32 ? 0xffffffffu : (1u << e) - 1u) & ~(f == 32 ? 0xffffffffu : (1u << f) - 1u);
+                const uint32_t pg = ids >> ((32 * lane) >> sh);
+                m &= page >= 32 ? ((pg & 1u) ? 0xffffffffu : 0u)
+                                : ((pg & 1u) ? 0xffffu : 0u) | ((pg & 2u) ? 0xffff0000u : 0u);
                 live_bits[s][lane] = m;
             }
             // whole multiples of 4 tokens, so that every copy is a multiple of 16 bytes
-            const int ntok = min(page, (r.len - pt + 3) & ~3);
+            const int ntok = min(page, (at.r.len - pt + 3) & ~3);
             const uint32_t bytes = id >= 0 ? static_cast<uint32_t>(ntok * unit) : 0u;
             const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);
             __syncwarp();
@@ -284,326 +363,354 @@ kv4_decode_kernel(const AttnParams p) {
             __syncwarp();
             if (bytes > 0)
                 bulk_load(ka_smem + s * L::kStage + dst0,
-                          base + ((static_cast<int64_t>(id) * p.c.heads + kvh) * page) * unit, bytes, &full_bar[s]);
+                          base + ((static_cast<int64_t>(id) * p.c.heads + at.kvh) * page) * unit, bytes, &full_bar[s]);
             issued = u - u0 + 1;
-            if (++s == kKaStages) { s = 0; ph ^= 1u; }
-            if (++ch == un.chunks) {
-                ch = 0;
-                if (++tile == un.tiles) {
-                    tile = 0;
-                    if (++kvh == p.c.heads) {
-                        kvh = 0;
-                        if (u + 1 < u1) {
-                            do {
-                                ++b;
-                                r = kv4_request(p, b);
-                                un = kv4_units<ROWS>(p, r);
-                            } while (un.tiles == 0);
-                        }
-                    }
-                }
-            }
+            if (++s == kStages) { s = 0; ph ^= 1u; }
+            at = ahead;
+            id = id_next;
         }
         // no copy may still be landing when the CTA exits
         if (lane == 0)
-            for (int64_t i = (issued > kKaStages ? issued - kKaStages : 0); i < issued; ++i)
-                mbar_wait(&full_bar[i % kKaStages], static_cast<uint32_t>(i / kKaStages) & 1u, nullptr, kDrainLimitNs);
-        return;
-    }
-
-    // -------------------------------------------------------------- consumers
-    const int g = lane >> 2, t = lane & 3;
-    const float c = p.scale_log2;
-    uint32_t qa[kSteps][kFull ? 4 : 2];
-    float acc[kNT][kFull ? 4 : 2];
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-    int lim0 = 0, lim1 = 0, low0 = 0, low1 = 0;     // rows g and g + 8 see the tokens low..lim
-    bool fresh = true, dead = false;
-    int seg = 0, seg_c0 = ch;
-    int s = 0;
-    uint32_t ph = 0;
-    float* const join = reinterpret_cast<float*>(ka_smem + kKaStages * L::kStage);
-
-    for (int64_t u = u0; u < u1; ++u) {
-        if (fresh) {
-            // a new tile: its queries in operand order, empty statistics
-            const int rows = r.nq * p.group;
-#pragma unroll
-            for (int h = 0; h < (kFull ? 2 : 1); ++h) {
-                const int row = tile * ROWS + g + 8 * h;
-                const bool in = row < rows;
-                const int tok = in ? row / p.group : 0;
-                const uint16_t* src = p.q + (r.q0 + tok) * p.q_stride +
-                                      static_cast<int64_t>(kvh * p.group + (in ? row - tok * p.group : 0)) * D + 8 * kW * t;
-#pragma unroll
-                for (int w = 0; w < kW; ++w) {
-                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                    if (in) x = __ldg(reinterpret_cast<const uint4*>(src) + w);
-                    qa[2 * w][h] = __byte_perm(x.x, x.z, 0x5410);
-                    qa[2 * w][(kFull ? 2 : 1) + h] = __byte_perm(x.x, x.z, 0x7632);
-                    qa[2 * w + 1][h] = __byte_perm(x.y, x.w, 0x5410);
-                    qa[2 * w + 1][(kFull ? 2 : 1) + h] = __byte_perm(x.y, x.w, 0x7632);
-                }
-                const int pos = r.first + tok;
-                // rows past the last query see everything: their zero queries are harmless, and masks stay rare
-                const int lim = !in ? 0x7fffffff : p.causal ? pos : r.len - 1;
-                const int low = in && p.window > 0 ? pos - p.window + 1 : 0;
-                if (h == 0) { lim0 = lim; low0 = low; } else { lim1 = lim; low1 = low; }
-            }
-#pragma unroll
-            for (int i = 0; i < kNT; ++i)
-#pragma unroll
-                for (int j = 0; j < (kFull ? 4 : 2); ++j) acc[i][j] = 0.0f;
-            m0 = m1 = -INFINITY;
-            l0 = l1 = 0.0f;
-            seg_c0 = ch;
-            fresh = false;
-        }
-        dead = dead || !mbar_wait(&full_bar[s], ph, abort, p.limit_ns);
-        dead = __any_sync(0xffffffffu, dead);
-        if (!dead) {
-            const uint32_t sb = ring + s * L::kStage;
-            const uint32_t live = live_bits[s][warp];
-            const int t0 = (un.c0 + ch) * kKaChunk + 32 * warp;       // first token of this warp's 32
-            // ---- S = Q K^T
-            float sv[4][kFull ? 4 : 2];
-            const uint32_t kbase = sb + (32 * warp + g) * (D / 2) + 4 * kW * t;
-            const uint32_t sbase = sb + 2 * L::kCodes + (32 * warp + g) * (D / 32) * 2 + 2 * (t * kW / 4);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t w[kW];
-                if (kW == 4) {
-                    const uint4 x = gm_lds128(kbase + j * 8 * (D / 2));
-                    w[0] = x.x; w[1] = x.y; w[2 % kW] = x.z; w[3 % kW] = x.w;
-                } else {
-                    const uint2 x = lds64(kbase + j * 8 * (D / 2));
-                    w[0] = x.x; w[1] = x.y;
-                }
-                const uint32_t st = lds_u16(sbase + j * 8 * (D / 32) * 2);
-                const uint32_t s2 = st | (st << 16), o2 = kv4_off(s2);
-                float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int i = 0; i < kW; ++i) {
-                    const uint32_t b0 = kv4_pair(w[i] << 3, s2, o2), b1 = kv4_pair(w[i] >> 1, s2, o2);
-                    const uint32_t b2 = kv4_pair(w[i] >> 5, s2, o2), b3 = kv4_pair(w[i] >> 9, s2, o2);
-                    if (kFull) {
-                        gm_mma(d, qa[2 * i][0], qa[2 * i][1], qa[2 * i][2 % (kFull ? 4 : 2)], qa[2 * i][3 % (kFull ? 4 : 2)], b0, b1);
-                        gm_mma(d, qa[2 * i + 1][0], qa[2 * i + 1][1], qa[2 * i + 1][2 % (kFull ? 4 : 2)],
-                               qa[2 * i + 1][3 % (kFull ? 4 : 2)], b2, b3);
-                    } else {
-                        gm_mma(d, qa[2 * i][0], 0u, qa[2 * i][1], 0u, b0, b1);
-                        gm_mma(d, qa[2 * i + 1][0], 0u, qa[2 * i + 1][1], 0u, b2, b3);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < (kFull ? 4 : 2); ++i) sv[j][i] = d[i];
-            }
-            // ---- masks: tokens that do not exist, and each row's own range
-            const int mn = kFull ? min(lim0, lim1) : lim0, mx = kFull ? max(low0, low1) : low0;
-            const bool plain = live == 0xffffffffu && mn >= t0 + 31 && mx <= t0;
-            if (!__all_sync(0xffffffffu, plain)) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int off = 8 * j + 2 * t + i, tk = t0 + off;
-                        const bool in = (live >> off) & 1u;
-                        if (!(in && tk <= lim0 && tk >= low0)) sv[j][i] = -INFINITY;
-                        if (kFull && !(in && tk <= lim1 && tk >= low1)) sv[j][(2 + i) % (kFull ? 4 : 2)] = -INFINITY;
-                    }
-            }
-            // ---- running maximum; outputs are rescaled only when it grows by more than 2^kKaGrow
-            float x0 = fmaxf(fmaxf(fmaxf(sv[0][0], sv[0][1]), fmaxf(sv[1][0], sv[1][1])),
-                             fmaxf(fmaxf(sv[2][0], sv[2][1]), fmaxf(sv[3][0], sv[3][1])));
-            float x1 = -INFINITY;
-            if (kFull) {
-                constexpr int a = 2 % (kFull ? 4 : 2), e = 3 % (kFull ? 4 : 2);
-                x1 = fmaxf(fmaxf(fmaxf(sv[0][a], sv[0][e]), fmaxf(sv[1][a], sv[1][e])),
-                           fmaxf(fmaxf(sv[2][a], sv[2][e]), fmaxf(sv[3][a], sv[3][e])));
-            }
-#pragma unroll
-            for (int d = 1; d <= 2; d <<= 1) {
-                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
-                if (kFull) x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
-            }
-            x0 *= c;
-            if (kFull) x1 *= c;
-            // m - x is NaN only for -inf - -inf: nothing seen yet, nothing to do
-            const bool grow0 = x0 > m0 + kKaGrow, grow1 = kFull && x1 > m1 + kKaGrow;
-            if (__any_sync(0xffffffffu, grow0 || grow1)) {
-                const float a0 = grow0 ? ex2(m0 - x0) : 1.0f, a1 = grow1 ? ex2(m1 - x1) : 1.0f;
-                if (grow0) m0 = x0;
-                if (grow1) m1 = x1;
-                l0 *= a0;
-                l1 *= a1;
-#pragma unroll
-                for (int i = 0; i < kNT; ++i) {
-                    acc[i][0] *= a0;
-                    acc[i][1] *= a0;
-                    if (kFull) {
-                        acc[i][2 % (kFull ? 4 : 2)] *= a1;
-                        acc[i][3 % (kFull ? 4 : 2)] *= a1;
-                    }
-                }
-            }
-            const float n0 = m0 == -INFINITY ? 0.0f : -m0, n1 = m1 == -INFINITY ? 0.0f : -m1;
-            uint32_t pa[2][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float e0 = ex2(fmaf(sv[j][0], c, n0)), e1 = ex2(fmaf(sv[j][1], c, n0));
-                l0 += e0 + e1;
-                pa[j >> 1][2 * (j & 1)] = pack_bf16(e0, e1);
-                if (kFull) {
-                    const float e2 = ex2(fmaf(sv[j][2 % (kFull ? 4 : 2)], c, n1));
-                    const float e3 = ex2(fmaf(sv[j][3 % (kFull ? 4 : 2)], c, n1));
-                    l1 += e2 + e3;
-                    pa[j >> 1][2 * (j & 1) + 1] = pack_bf16(e2, e3);
-                } else {
-                    pa[j >> 1][2 * (j & 1) + 1] = 0u;
-                }
-            }
-            // ---- O += P V
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t bp[2][8 * kVW];                     // pairs of tokens (2t, 2t+1) and (2t+8, 2t+9)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int off = 16 * k + 8 * h + 2 * t;
-                    const uint32_t vb = sb + L::kCodes + (32 * warp + off) * (D / 2) + 4 * kVW * g;
-                    const uint32_t ss = sb + 2 * L::kCodes + L::kSteps + (32 * warp + off) * (D / 32) * 2 + 2 * (kVW * g / 4);
-                    uint32_t wa[kVW], wb[kVW];
-                    if (kVW == 2) {
-                        const uint2 xa = lds64(vb), xb = lds64(vb + D / 2);
-                        wa[0] = xa.x; wa[1 % kVW] = xa.y;
-                        wb[0] = xb.x; wb[1 % kVW] = xb.y;
-                    } else {
-                        wa[0] = gm_lds32(vb);
-                        wb[0] = gm_lds32(vb + D / 2);
-                    }
-                    uint32_t s2 = __byte_perm(lds_u16(ss), lds_u16(ss + (D / 32) * 2), 0x5410);
-                    if (live != 0xffffffffu)                   // tokens that do not exist: step 0
-                        s2 &= (((live >> off) & 1u) ? 0xffffu : 0u) | (((live >> (off + 1)) & 1u) ? 0xffff0000u : 0u);
-                    const uint32_t o2 = kv4_off(s2);
-#pragma unroll
-                    for (int i = 0; i < kVW; ++i) {
-                        const uint32_t lo = __byte_perm(wa[i], wb[i], 0x5410), hi = __byte_perm(wa[i], wb[i], 0x7632);
-                        bp[h][8 * i + 0] = kv4_pair(lo << 3, s2, o2);
-                        bp[h][8 * i + 1] = kv4_pair(lo >> 1, s2, o2);
-                        bp[h][8 * i + 2] = kv4_pair(lo >> 5, s2, o2);
-                        bp[h][8 * i + 3] = kv4_pair(lo >> 9, s2, o2);
-                        bp[h][8 * i + 4] = kv4_pair(hi << 3, s2, o2);
-                        bp[h][8 * i + 5] = kv4_pair(hi >> 1, s2, o2);
-                        bp[h][8 * i + 6] = kv4_pair(hi >> 5, s2, o2);
-                        bp[h][8 * i + 7] = kv4_pair(hi >> 9, s2, o2);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kNT; ++i) {
-                    if constexpr (kFull) {
-                        gm_mma(acc[i], pa[k][0], pa[k][1], pa[k][2], pa[k][3], bp[0][i], bp[1][i]);
-                    } else {
-                        float d[4] = {acc[i][0], acc[i][1], 0.0f, 0.0f};
-                        gm_mma(d, pa[k][0], 0u, pa[k][2], 0u, bp[0][i], bp[1][i]);
-                        acc[i][0] = d[0];
-                        acc[i][1] = d[1];
-                    }
-                }
-            }
-        }
-        // the slot is released only once what was loaded from it has been used
+            for (int64_t i = (issued > kStages ? issued - kStages : 0); i < issued; ++i)
+                mbar_wait(&full_bar[i % kStages], static_cast<uint32_t>(i / kStages) & 1u, nullptr, kDrainLimitNs);
         __syncwarp();
-        if (lane == 0 && !dead) mbar_arrive(&empty_bar[s]);
-        if (++s == kKaStages) { s = 0; ph ^= 1u; }
+    } else {
+        // ---------------------------------------------------------- consumers
+        const int g = lane >> 2, t = lane & 3;
+        const float c = p.scale_log2;
+        uint32_t qb[kN][2 * kW][2];                 // q of row 8n + g, this thread's channels, operand order
+        float acc[kM][kN][4];
+        float m[kN][2], l[kN][2];                   // of rows 8n + 2t and 8n + 2t + 1: reference maximum, sum
+        int lim[kN][2], low[kN][2];                 // these rows see the tokens low..lim
+        bool fresh = true, dead = false;
+        int seg = 0, seg_c0 = at.ch;
+        int s = 0;
+        uint32_t ph = 0;
+        float* const join = reinterpret_cast<float*>(ka_smem + kStages * L::kStage);
 
-        const bool tile_end = ch == un.chunks - 1;
-        if (tile_end || u == u1 - 1) {
-            // ---- join the four warps, then write the rows or leave the piece in the workspace
+        for (int64_t u = u0; u < u1; ++u) {
+            if (fresh) {
+                // a new tile: its queries in operand order, empty statistics
+                const int rows = at.r.nq * p.group;
 #pragma unroll
-            for (int d = 1; d <= 2; d <<= 1) {
-                l0 += __shfl_xor_sync(0xffffffffu, l0, d);
-                if (kFull) l1 += __shfl_xor_sync(0xffffffffu, l1, d);
-            }
-            if (t == 0) {
-                join_m[warp][g] = m0;
-                join_l[warp][g] = l0;
-                if (kFull) {
-                    join_m[warp][g + 8] = m1;
-                    join_l[warp][g + 8] = l1;
+                for (int n = 0; n < kN; ++n) {
+                    const int row = at.tile * ROWS + 8 * n + g;
+                    const bool in = row < rows && (!kLo || g < 4);
+                    const int tok = in ? row / p.group : 0;
+                    const uint16_t* src = p.q + (at.r.q0 + tok) * p.q_stride +
+                                          static_cast<int64_t>(at.kvh * p.group + (in ? row - tok * p.group : 0)) * D + 8 * kW * t;
+#pragma unroll
+                    for (int w = 0; w < kW; ++w) {
+                        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                        if (in) x = __ldg(reinterpret_cast<const uint4*>(src) + w);
+                        qb[n][2 * w][0] = __byte_perm(x.x, x.z, 0x5410);
+                        qb[n][2 * w][1] = __byte_perm(x.x, x.z, 0x7632);
+                        qb[n][2 * w + 1][0] = __byte_perm(x.y, x.w, 0x5410);
+                        qb[n][2 * w + 1][1] = __byte_perm(x.y, x.w, 0x7632);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int rr = at.tile * ROWS + 8 * n + 2 * t + e;
+                        const bool there = rr < rows && (!kLo || t < 2);
+                        const int pos = at.r.first + (there ? rr / p.group : 0);
+                        // rows that do not exist see everything: their zero queries are harmless, and masks stay rare
+                        lim[n][e] = !there ? 0x7fffffff : p.causal ? pos : at.r.len - 1;
+                        low[n][e] = there && p.window > 0 ? pos - p.window + 1 : 0;
+                        m[n][e] = -INFINITY;
+                        l[n][e] = 0.0f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kM; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[i][n][j] = 0.0f;
                 }
+                seg_c0 = at.ch;
+                fresh = false;
             }
+            dead = dead || !mbar_wait(&full_bar[s], ph, abort, p.limit_ns);
+            dead = __any_sync(0xffffffffu, dead);
+            if (!dead) {
+                const uint32_t sb = ring + s * L::kStage;
+                const uint32_t live = live_bits[s][warp];
+                const int t0 = at.t0() + 32 * warp;                  // first token of this warp's 32
+                // ---- S^T = K Q^T, two tiles of 16 tokens
+                float sv[2][kN][4];
+                const uint32_t kbase = sb + (32 * warp + g) * (D / 2) + 4 * kW * t;
+                const uint32_t sbase = sb + 2 * L::kCodes + (32 * warp + g) * (D / 32) * 2 + 2 * (t * kW / 4);
 #pragma unroll
-            for (int h = 0; h < (kFull ? 2 : 1); ++h) {
-                float* o = join + (warp * ROWS + g + 8 * h) * (L::kORow / 4) + 16 * kVW * t;
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t w[2][kW], s2[2], o2[2];                 // tokens g and g + 8 of the tile
 #pragma unroll
-                for (int cc = 0; cc < 2; ++cc)                 // accumulator column: channels +0.. or + 8 kVW..
+                    for (int h = 0; h < 2; ++h) {
+                        if (kW == 4) {
+                            const uint4 x = gm_lds128(kbase + (16 * k + 8 * h) * (D / 2));
+                            w[h][0] = x.x; w[h][1] = x.y; w[h][2 % kW] = x.z; w[h][3 % kW] = x.w;
+                        } else {
+                            const uint2 x = lds64(kbase + (16 * k + 8 * h) * (D / 2));
+                            w[h][0] = x.x; w[h][1] = x.y;
+                        }
+                        s2[h] = __byte_perm(lds_u16(sbase + (16 * k + 8 * h) * (D / 32) * 2), 0u, 0x1010);
+                        o2[h] = kv4_off(s2[h]);
+                    }
 #pragma unroll
-                    for (int i = 0; i < 8 * kVW; i += 4)
-                        *reinterpret_cast<float4*>(o + cc * 8 * kVW + i) =
-                            make_float4(acc[i][(2 * h + cc) % (kFull ? 4 : 2)], acc[i + 1][(2 * h + cc) % (kFull ? 4 : 2)],
-                                        acc[i + 2][(2 * h + cc) % (kFull ? 4 : 2)], acc[i + 3][(2 * h + cc) % (kFull ? 4 : 2)]);
-            }
-            asm volatile("bar.sync 1, %0;" :: "n"(32 * kKaWarps) : "memory");
-            const int rows = r.nq * p.group - tile * ROWS;     // rows of this tile that exist
-            const bool whole = seg_c0 == 0 && tile_end;
-            const int slot = 2 * static_cast<int>(blockIdx.x) + (seg > 0 ? 1 : 0);
-            float* const piece = p.part + static_cast<int64_t>(slot) * ka_piece<D, ROWS>();
-            constexpr int kPer = D / 8;                         // threads per row: 8 channels each
-            for (int x = tid; x < ROWS * kPer; x += 32 * kKaWarps) {
-                const int row = x / kPer, d0 = (x - row * kPer) * 8;
-                if (row >= rows) break;
-                float mm = -INFINITY;
+                    for (int i = 0; i < kW; ++i) {
+                        uint32_t a[2][4];
 #pragma unroll
-                for (int w = 0; w < kKaWarps; ++w) mm = fmaxf(mm, join_m[w][row]);
-                float ll = 0.0f, o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+                        for (int h = 0; h < 2; ++h) {
+                            a[0][h] = kv4_pair(w[h][i] << 3, s2[h], o2[h]);
+                            a[0][2 + h] = kv4_pair(w[h][i] >> 1, s2[h], o2[h]);
+                            a[1][h] = kv4_pair(w[h][i] >> 5, s2[h], o2[h]);
+                            a[1][2 + h] = kv4_pair(w[h][i] >> 9, s2[h], o2[h]);
+                        }
 #pragma unroll
-                for (int w = 0; w < kKaWarps; ++w) {
-                    const float f = mm == -INFINITY ? 0.0f : ex2(join_m[w][row] - mm);
-                    ll += f * join_l[w][row];
-                    const float4* src = reinterpret_cast<const float4*>(join + (w * ROWS + row) * (L::kORow / 4) + d0);
-                    const float4 a = src[0], e = src[1];
-                    o[0] += f * a.x; o[1] += f * a.y; o[2] += f * a.z; o[3] += f * a.w;
-                    o[4] += f * e.x; o[5] += f * e.y; o[6] += f * e.z; o[7] += f * e.w;
-                }
-                if (*abort) continue;
-                if (whole) {
-                    const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
-                    const int64_t at = ka_out_row(p, r, kvh, tile * ROWS + row);
-                    *reinterpret_cast<uint4*>(p.out + at * D + d0) =
-                        make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
-                                   pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
-                    if (d0 == 0 && p.lse) p.lse[at] = ll > 0.0f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
-                } else {
-                    float4* dst = reinterpret_cast<float4*>(piece + row * D + d0);
-                    dst[0] = make_float4(o[0], o[1], o[2], o[3]);
-                    dst[1] = make_float4(o[4], o[5], o[6], o[7]);
-                    if (d0 == 0) {
-                        piece[ROWS * D + row] = mm;
-                        piece[ROWS * D + ROWS + row] = ll;
+                        for (int n = 0; n < kN; ++n) {
+                            if (i == 0) ka_mma0(sv[k][n], a[0][0], a[0][1], a[0][2], a[0][3], qb[n][0][0], qb[n][0][1]);
+                            else gm_mma(sv[k][n], a[0][0], a[0][1], a[0][2], a[0][3], qb[n][2 * i][0], qb[n][2 * i][1]);
+                            gm_mma(sv[k][n], a[1][0], a[1][1], a[1][2], a[1][3], qb[n][2 * i + 1][0], qb[n][2 * i + 1][1]);
+                        }
                     }
                 }
-            }
-            if (!whole && tid == 0)
-                meta[seg > 0 ? 1 : 0] = make_int4(b, kvh * un.tiles + tile, seg_c0, ch + 1 == un.chunks ? -(ch + 1) : ch + 1);
-            asm volatile("bar.sync 1, %0;" :: "n"(32 * kKaWarps) : "memory");
-            fresh = true;
-            ++seg;
-        }
-        if (++ch == un.chunks) {
-            ch = 0;
-            if (++tile == un.tiles) {
-                tile = 0;
-                if (++kvh == p.c.heads) {
-                    kvh = 0;
-                    if (u + 1 < u1) {
-                        do {
-                            ++b;
-                            r = kv4_request(p, b);
-                            un = kv4_units<ROWS>(p, r);
-                        } while (un.tiles == 0);
+                // ---- masks: tokens that do not exist, and each row's own range
+                bool plain = live == 0xffffffffu;
+#pragma unroll
+                for (int n = 0; n < kN; ++n)
+                    plain = plain && min(lim[n][0], lim[n][1]) >= t0 + 31 && max(low[n][0], low[n][1]) <= t0;
+                if (!__all_sync(0xffffffffu, plain)) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int n = 0; n < kN; ++n)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int off = 16 * k + g + 8 * (i >> 1), tk = t0 + off;
+                                if (!((live >> off) & 1u) || tk > lim[n][i & 1] || tk < low[n][i & 1]) sv[k][n][i] = -INFINITY;
+                            }
+                }
+                // ---- reference maxima move, and outputs are rescaled, only when a score exceeds them by 2^kKaGrow
+                float x[kN][2];
+                bool grow = false;
+#pragma unroll
+                for (int n = 0; n < kN; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        x[n][e] = fmaxf(fmaxf(sv[0][n][e], sv[0][n][2 + e]), fmaxf(sv[1][n][e], sv[1][n][2 + e])) * c;
+                        grow = grow || x[n][e] > m[n][e] + kKaGrow;
                     }
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int n = 0; n < kN; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float y = x[n][e];
+#pragma unroll
+                            for (int d = 4; d <= 16; d <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
+                            const bool up = y > m[n][e] + kKaGrow;      // the same in the row's 8 lanes
+                            float a = up ? ex2(m[n][e] - y) : 1.0f;
+                            if (up) m[n][e] = y;
+                            l[n][e] *= a;
+                            if (kLo) {                                  // the remainders' columns go with their rows
+                                const float b = __shfl_xor_sync(0xffffffffu, a, 2);
+                                if (t >= 2) a = b;
+                            }
+#pragma unroll
+                            for (int i = 0; i < kM; ++i) {
+                                acc[i][n][e] *= a;
+                                acc[i][n][2 + e] *= a;
+                            }
+                        }
+                }
+                // ---- P, transposed into the second product's operand
+                uint32_t pb[2][kN][2];
+#pragma unroll
+                for (int n = 0; n < kN; ++n) {
+                    const float n0 = m[n][0] == -INFINITY ? 0.0f : -m[n][0], n1 = m[n][1] == -INFINITY ? 0.0f : -m[n][1];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float e0 = ex2(fmaf(sv[k][n][2 * h], c, n0)), e1 = ex2(fmaf(sv[k][n][2 * h + 1], c, n1));
+                            l[n][0] += e0;
+                            l[n][1] += e1;
+                            uint32_t hi = pack_bf16(e0, e1);
+                            if (kLo) {
+                                const uint32_t lo = __shfl_xor_sync(
+                                    0xffffffffu, pack_bf16(e0 - __uint_as_float(hi << 16), e1 - __uint_as_float(hi & 0xFFFF0000u)), 2);
+                                if (t >= 2) hi = lo;
+                            }
+                            pb[k][n][h] = ka_trans(hi);
+                        }
+                }
+                // ---- O^T += V^T P^T
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t v[2][8 * kVW];                  // pairs of tokens (2t, 2t+1) and (2t+8, 2t+9)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int off = 16 * k + 8 * h + 2 * t;
+                        const uint32_t vb = sb + L::kCodes + (32 * warp + off) * (D / 2) + 4 * kVW * g;
+                        const uint32_t ss = sb + 2 * L::kCodes + L::kSteps + (32 * warp + off) * (D / 32) * 2 + 2 * (kVW * g / 4);
+                        uint32_t wa[kVW], wb[kVW];
+                        if (kVW == 2) {
+                            const uint2 xa = lds64(vb), xb = lds64(vb + D / 2);
+                            wa[0] = xa.x; wa[1 % kVW] = xa.y;
+                            wb[0] = xb.x; wb[1 % kVW] = xb.y;
+                        } else {
+                            wa[0] = gm_lds32(vb);
+                            wb[0] = gm_lds32(vb + D / 2);
+                        }
+                        uint32_t s2 = __byte_perm(lds_u16(ss), lds_u16(ss + (D / 32) * 2), 0x5410);
+                        if (live != 0xffffffffu)               // tokens that do not exist: step 0
+                            s2 &= (((live >> off) & 1u) ? 0xffffu : 0u) | (((live >> (off + 1)) & 1u) ? 0xffff0000u : 0u);
+                        const uint32_t o2 = kv4_off(s2);
+#pragma unroll
+                        for (int i = 0; i < kVW; ++i) {
+                            const uint32_t lo = __byte_perm(wa[i], wb[i], 0x5410), hi = __byte_perm(wa[i], wb[i], 0x7632);
+                            v[h][8 * i + 0] = kv4_pair(lo << 3, s2, o2);
+                            v[h][8 * i + 1] = kv4_pair(lo >> 1, s2, o2);
+                            v[h][8 * i + 2] = kv4_pair(lo >> 5, s2, o2);
+                            v[h][8 * i + 3] = kv4_pair(lo >> 9, s2, o2);
+                            v[h][8 * i + 4] = kv4_pair(hi << 3, s2, o2);
+                            v[h][8 * i + 5] = kv4_pair(hi >> 1, s2, o2);
+                            v[h][8 * i + 6] = kv4_pair(hi >> 5, s2, o2);
+                            v[h][8 * i + 7] = kv4_pair(hi >> 9, s2, o2);
+                        }
+                    }
+                    // rows g and g + 8 of tile i: this thread's channels i and i + kM
+#pragma unroll
+                    for (int i = 0; i < kM; ++i)
+#pragma unroll
+                        for (int n = 0; n < kN; ++n)
+                            gm_mma(acc[i][n], v[0][i], v[0][kM + i], v[1][i], v[1][kM + i], pb[k][n][0], pb[k][n][1]);
                 }
             }
+            // the slot is released only once what was loaded from it has been used
+            __syncwarp();
+            if (lane == 0 && !dead) mbar_arrive(&empty_bar[s]);
+            if (++s == kStages) { s = 0; ph ^= 1u; }
+
+            const bool tile_end = at.ch == at.un.chunks - 1;
+            if (tile_end || u == u1 - 1) {
+                // ---- join the four warps, then write the rows or leave the piece to be joined with others
+#pragma unroll
+                for (int n = 0; n < kN; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int d = 4; d <= 16; d <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
+                        if (g == 0 && (!kLo || t < 2)) {
+                            join_m[warp][8 * n + 2 * t + e] = m[n][e];
+                            join_l[warp][8 * n + 2 * t + e] = l[n][e];
+                        }
+                        float o[2 * kM];                      // the row's channels 2 kM g ..
+#pragma unroll
+                        for (int i = 0; i < kM; ++i) {
+                            o[i] = acc[i][n][e];
+                            o[kM + i] = acc[i][n][2 + e];
+                        }
+                        if (kLo) {
+#pragma unroll
+                            for (int i = 0; i < 2 * kM; ++i) o[i] += __shfl_xor_sync(0xffffffffu, o[i], 2);
+                        }
+                        if (!kLo || t < 2) {
+                            float4* dst = reinterpret_cast<float4*>(join + (warp * ROWS + 8 * n + 2 * t + e) * (L::kORow / 4) + 2 * kM * g);
+#pragma unroll
+                            for (int i = 0; i < kM / 2; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        }
+                    }
+                asm volatile("bar.sync 1, %0;" :: "n"(32 * kKaWarps) : "memory");
+                const int rows = at.r.nq * p.group - at.tile * ROWS;     // rows of this tile that exist
+                const bool whole = !CL && seg_c0 == 0 && tile_end;
+                const int slot = 2 * static_cast<int>(blockIdx.x) + (seg > 0 ? 1 : 0);
+                float* const piece = CL ? res : p.part + static_cast<int64_t>(slot) * ka_piece<D, ROWS>();
+                constexpr int kPer = D / 8;                             // threads per row: 8 channels each
+                for (int x = tid; x < ROWS * kPer; x += 32 * kKaWarps) {
+                    const int row = x / kPer, d0 = (x - row * kPer) * 8;
+                    if (row >= rows) break;
+                    float mm = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < kKaWarps; ++w) mm = fmaxf(mm, join_m[w][row]);
+                    float ll = 0.0f, o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int w = 0; w < kKaWarps; ++w) {
+                        const float f = mm == -INFINITY ? 0.0f : ex2(join_m[w][row] - mm);
+                        ll += f * join_l[w][row];
+                        const float4* src = reinterpret_cast<const float4*>(join + (w * ROWS + row) * (L::kORow / 4) + d0);
+                        const float4 a = src[0], e = src[1];
+                        o[0] += f * a.x; o[1] += f * a.y; o[2] += f * a.z; o[3] += f * a.w;
+                        o[4] += f * e.x; o[5] += f * e.y; o[6] += f * e.z; o[7] += f * e.w;
+                    }
+                    if (*abort) continue;
+                    if (whole) {
+                        const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+                        const int64_t to = ka_out_row(p, at.r, at.kvh, at.tile * ROWS + row);
+                        *reinterpret_cast<uint4*>(p.out + to * D + d0) =
+                            make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
+                                       pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
+                        if (d0 == 0 && p.lse) p.lse[to] = ll > 0.0f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(piece + row * D + d0);
+                        dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+                        dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+                        if (d0 == 0) {
+                            piece[ROWS * D + row] = mm;
+                            piece[ROWS * D + ROWS + row] = ll;
+                        }
+                    }
+                }
+                if (!CL && !whole && tid == 0)
+                    p.meta[2 * blockIdx.x + (seg > 0 ? 1 : 0)] =
+                        make_int4(at.b, at.kvh * at.un.tiles + at.tile, seg_c0, tile_end ? -(at.ch + 1) : at.ch + 1);
+                asm volatile("bar.sync 1, %0;" :: "n"(32 * kKaWarps) : "memory");
+                fresh = true;
+                ++seg;
+            }
+            if (u + 1 < u1) at.next(p, true);
         }
+        if (CL && u0 >= u1) {
+            // no chunk for this CTA: an empty piece
+            for (int x = tid; x < ka_piece<D, ROWS>(); x += 32 * kKaWarps)
+                res[x] = x >= ROWS * D && x < ROWS * D + ROWS ? -INFINITY : 0.0f;
+        }
+    }
+    if (CL) {
+        // ---- the cluster's pieces joined: each CTA takes its share of (row, 4 channels)
+        __syncwarp();
+        cluster_sync_all();
+        const int rank = static_cast<int>(cluster_ctarank());
+        // the place of the tile (the roles above may have moved on)
+        const Request r = kv4_request(p, s_b);
+        const Units<ROWS> un = kv4_units<ROWS>(p, r);
+        const int kvh = static_cast<int>(s_skip / un.tiles), tile = static_cast<int>(s_skip % un.tiles);
+        const int rows = r.nq * p.group - tile * ROWS;
+        constexpr int kPer = D / 4, kShare = ROWS * kPer / kKaCluster;
+        const int x = rank * kShare + tid, row = x / kPer, d0 = (x - row * kPer) * 4;
+        if (tid < kShare && row < rows && !*abort) {
+            uint32_t from[kKaCluster];
+            float mj[kKaCluster], mm = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < kKaCluster; ++j) {
+                from[j] = cluster_map(res, j);
+                mj[j] = ld_cluster_f32(from[j] + (ROWS * D + row) * 4);
+            }
+#pragma unroll
+            for (int j = 0; j < kKaCluster; ++j) mm = fmaxf(mm, mj[j]);
+            float ll = 0.0f;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int j = 0; j < kKaCluster; ++j) {
+                const float f = mm == -INFINITY ? 0.0f : ex2(mj[j] - mm);
+                const float4 v = ld_cluster_f32x4(from[j] + (row * D + d0) * 4);
+                ll += f * ld_cluster_f32(from[j] + (ROWS * D + ROWS + row) * 4);
+                o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
+            }
+            const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+            const int64_t to = ka_out_row(p, r, kvh, tile * ROWS + row);
+            *reinterpret_cast<uint2*>(p.out + to * D + d0) =
+                make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+            if (d0 == 0 && p.lse) p.lse[to] = ll > 0.0f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+        }
+        __syncwarp();
+        cluster_sync_all();      // no CTA leaves while another may still read its piece
     }
 }
 

@@ -866,18 +866,22 @@ static qat4::Kv4View kv4_view(const qat4_kv4_cache* c) {
 
 // A launch that may overlap the end of the kernel before it in the stream (each of these kernels
 // waits for that kernel before it touches memory).
+// `cluster`: CTAs per cluster along x.
 template <typename... P, typename... A>
-static bool launch_pdl(void (*kernel)(P...), dim3 grid, int block, size_t smem, cudaStream_t stream, A... args) {
-    cudaLaunchAttribute pdl[1];
+static bool launch_pdl(void (*kernel)(P...), dim3 grid, int block, size_t smem, cudaStream_t stream, int cluster, A... args) {
+    cudaLaunchAttribute pdl[2];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    pdl[1].id = cudaLaunchAttributeClusterDimension;
+    pdl[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    pdl[1].val.clusterDim.y = pdl[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(block));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = pdl;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
@@ -888,7 +892,8 @@ static bool smem_attr(K kernel, size_t bytes) {
 
 template <int D, int ROWS>
 static bool kv4_decode_attr() {
-    return smem_attr(qat4::kv4_decode_kernel<D, ROWS>, qat4::KaLayout<D, ROWS>::kSmem);
+    return smem_attr(qat4::kv4_decode_kernel<D, ROWS, false>, qat4::KaLayout<D, ROWS>::kSmem) &&
+           smem_attr(qat4::kv4_decode_kernel<D, ROWS, true>, qat4::KaLayout<D, ROWS>::kSmem);
 }
 
 // The prefill kernel's warpgroups trade registers: their shares must fit what the block is launched with, or
@@ -906,8 +911,8 @@ static bool kv4_attrs(DeviceInfo* info) {
     std::lock_guard<std::mutex> lock(g_mutex);
     if (info->kv4_attr) return true;
     if (!smem_attr(qat4::kv4_tables_kernel, qat4::tables_smem_bytes(qat4::kTbMaxRequests))) return false;
-    if (!kv4_decode_attr<64, 8>() || !kv4_decode_attr<64, 16>() || !kv4_decode_attr<128, 8>() ||
-        !kv4_decode_attr<128, 16>())
+    if (!kv4_decode_attr<64, 4>() || !kv4_decode_attr<64, 8>() || !kv4_decode_attr<64, 16>() ||
+        !kv4_decode_attr<128, 4>() || !kv4_decode_attr<128, 8>() || !kv4_decode_attr<128, 16>())
         return false;
     if (!kv4_prefill_attr<64>() || !kv4_prefill_attr<128>()) return false;
     info->kv4_attr = true;
@@ -966,7 +971,7 @@ qat4_status qat4_kv4_tables(const int32_t* lengths, const int32_t* new_lengths, 
     // four tokens per thread, and a warp for every few requests
     const int64_t want = std::max((num_slots + 4 * qat4::kTbThreads - 1) / (4 * qat4::kTbThreads), (B + 63) / 64);
     const unsigned grid = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(want, info->sms)));
-    return launch_pdl(qat4::kv4_tables_kernel, dim3(grid), qat4::kTbThreads, qat4::tables_smem_bytes(p.B), stream, p)
+    return launch_pdl(qat4::kv4_tables_kernel, dim3(grid), qat4::kTbThreads, qat4::tables_smem_bytes(p.B), stream, 1, p)
                ? QAT4_OK : QAT4_ERR_CUDA;
 }
 
@@ -989,8 +994,8 @@ qat4_status qat4_kv4_append(const qat4_kv4_cache* cache, const void* k, const vo
     const dim3 grid(static_cast<unsigned>((2 * items + qat4::kKvBlock - 1) / qat4::kKvBlock));
     const qat4::Kv4View c = kv4_view(cache);
     const bool ok = dtype == QAT4_BF16
-        ? launch_pdl(qat4::kv4_append_kernel<true>, grid, qat4::kKvBlock, 0, stream, c, k, v, k_stride, v_stride, slots, items)
-        : launch_pdl(qat4::kv4_append_kernel<false>, grid, qat4::kKvBlock, 0, stream, c, k, v, k_stride, v_stride, slots, items);
+        ? launch_pdl(qat4::kv4_append_kernel<true>, grid, qat4::kKvBlock, 0, stream, 1, c, k, v, k_stride, v_stride, slots, items)
+        : launch_pdl(qat4::kv4_append_kernel<false>, grid, qat4::kKvBlock, 0, stream, 1, c, k, v, k_stride, v_stride, slots, items);
     return ok ? QAT4_OK : QAT4_ERR_CUDA;
 }
 
@@ -1005,17 +1010,16 @@ qat4_status qat4_kv4_gather(const qat4_kv4_cache* cache, const int32_t* slots, i
     if (n == 0) return QAT4_OK;
     const int64_t items = n * (row / 8);
     const dim3 grid(static_cast<unsigned>((2 * items + qat4::kKvBlock - 1) / qat4::kKvBlock));
-    return launch_pdl(qat4::kv4_gather_kernel, grid, qat4::kKvBlock, 0, stream, kv4_view(cache), slots, items, k, v)
+    return launch_pdl(qat4::kv4_gather_kernel, grid, qat4::kKvBlock, 0, stream, 1, kv4_view(cache), slots, items, k, v)
                ? QAT4_OK : QAT4_ERR_CUDA;
 }
 
 }  // extern "C"
 
-// Grid of the decode kernel: two CTAs per SM of a B200, and SMs for the split of the prefill kernel.  The same
-// numbers on any device, so that the workspace size does not depend on it; a device with fewer SMs runs the
-// CTAs in waves.
+// SMs of a B200, for the grid of the decode kernel and the split of the prefill kernel: the same number on any
+// device, so that the workspace size does not depend on it; a device with fewer SMs runs the CTAs in waves.
 static constexpr int kKaSms = 148;
-static constexpr int kKaGrid = 2 * kKaSms;
+static constexpr int kKaGrid = 3 * kKaSms;       // most CTAs of the decode kernel
 
 // Which kernels serve a call, from what the host knows of it: N query tokens of B requests.
 //   average rows per request and kv head <= 32: the decode kernel takes every request (decode steps, drafts);
@@ -1060,20 +1064,35 @@ extern "C" size_t qat4_kv4_attention_workspace_bytes(int64_t N, int64_t B, int64
     return bytes;
 }
 
+// tiles: upper bound of the row tiles over all kv heads; chunks: most chunks of a request.
 template <int D, int ROWS>
-static bool kv4_decode_launch(const qat4::AttnParams& p, cudaStream_t stream) {
-    return launch_pdl(qat4::kv4_decode_kernel<D, ROWS>, dim3(kKaGrid), qat4::kKaThreads, qat4::KaLayout<D, ROWS>::kSmem,
-                      stream, p) &&
-           launch_pdl(qat4::kv4_combine_kernel<D, ROWS>, dim3(kKaGrid, 4), qat4::kKcThreads, 0, stream, p, kKaGrid);
+static bool kv4_decode_launch(const qat4::AttnParams& p, int64_t chunks, cudaStream_t stream) {
+    using L = qat4::KaLayout<D, ROWS>;
+    const int64_t rows = static_cast<int64_t>(p.N) * p.group;
+    const int64_t tiles = (rows / ROWS + std::min<int64_t>(p.B, rows)) * p.c.heads;
+    if (tiles * qat4::kKaCluster <= kKaGrid && chunks <= 4 * qat4::kKaCluster)
+        return launch_pdl(qat4::kv4_decode_kernel<D, ROWS, true>, dim3(static_cast<unsigned>(tiles * qat4::kKaCluster)),
+                          qat4::kKaThreads, L::kSmem, stream, qat4::kKaCluster, p);
+    const int grid = kKaSms * L::kPerSm;
+    return launch_pdl(qat4::kv4_decode_kernel<D, ROWS, false>, dim3(grid), qat4::kKaThreads, L::kSmem, stream, 1, p) &&
+           launch_pdl(qat4::kv4_combine_kernel<D, ROWS>, dim3(grid, 4), qat4::kKcThreads, 0, stream, 1, p, grid);
+}
+
+template <int D>
+static bool kv4_decode_rows(const qat4::AttnParams& p, int64_t chunks, cudaStream_t stream) {
+    const int64_t rows = static_cast<int64_t>(p.N) * p.group;      // tiles as tall as the average request's rows
+    return rows <= 4 * static_cast<int64_t>(p.B) ? kv4_decode_launch<D, 4>(p, chunks, stream)
+         : rows <= 8 * static_cast<int64_t>(p.B) ? kv4_decode_launch<D, 8>(p, chunks, stream)
+                                                 : kv4_decode_launch<D, 16>(p, chunks, stream);
 }
 
 template <int D>
 static bool kv4_prefill_launch(const qat4::PrefillParams& p, int64_t tiles, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>(tiles * p.a.c.heads), static_cast<unsigned>(p.splits));
-    if (!launch_pdl(qat4::kv4_prefill_kernel<D>, grid, qat4::kKpThreads, qat4::KpLayout<D>::kSmem, stream, p)) return false;
+    if (!launch_pdl(qat4::kv4_prefill_kernel<D>, grid, qat4::kKpThreads, qat4::KpLayout<D>::kSmem, stream, 1, p)) return false;
     if (p.splits == 1) return true;
     const int64_t rows = static_cast<int64_t>(p.a.N) * p.a.Hq;
-    return launch_pdl(qat4::kv4_join_kernel<D>, dim3(static_cast<unsigned>((rows + 7) / 8)), qat4::kKjThreads, 0, stream, p);
+    return launch_pdl(qat4::kv4_join_kernel<D>, dim3(static_cast<unsigned>((rows + 7) / 8)), qat4::kKjThreads, 0, stream, 1, p);
 }
 
 extern "C" {
@@ -1128,9 +1147,8 @@ qat4_status qat4_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t N, i
     if (pl.decode) {
         p.rows_lo = pl.lo_decode;
         p.rows_hi = pl.hi_decode;
-        const bool half = N * p.group <= 8 * B;      // tiles of 8 rows where the average request has no more
-        ok = D == 64 ? (half ? kv4_decode_launch<64, 8>(p, stream) : kv4_decode_launch<64, 16>(p, stream))
-                     : (half ? kv4_decode_launch<128, 8>(p, stream) : kv4_decode_launch<128, 16>(p, stream));
+        const int64_t chunks = (max_blocks * cache->page_size + qat4::kKaChunk - 1) / qat4::kKaChunk;
+        ok = D == 64 ? kv4_decode_rows<64>(p, chunks, stream) : kv4_decode_rows<128>(p, chunks, stream);
     }
     if (ok && pl.prefill) {
         qat4::PrefillParams pp;
