@@ -149,10 +149,10 @@ struct KaLayout {
     static constexpr int kCodes = kKaChunk * D / 2;
     static constexpr int kSteps = kKaChunk * (D / 32) * 2;
     static constexpr int kStage = 2 * kCodes + 2 * kSteps;
-    static constexpr int kStages = 4;                             // 73 KB of ring at D = 128
+    static constexpr int kPerSm = ROWS == 16 ? 2 : 3;             // CTAs per SM (registers, shared memory)
+    static constexpr int kStages = kPerSm == 3 ? 3 : 4;           // 55 or 73 KB of ring at D = 128
     static constexpr int kORow = D * 4 + 16;                      // bytes of an output row in the join buffer
     static constexpr int kJoin = kKaWarps * ROWS * kORow;
-    static constexpr int kPerSm = ROWS == 16 || D == 128 ? 2 : 3; // CTAs per SM (registers, shared memory)
     static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStage + kJoin;
 };
 
@@ -717,15 +717,17 @@ kv4_decode_kernel(const AttnParams p) {
 // Joins the pieces of a cut tile.  Records: (request, kvh * tiles + tile, first chunk, end chunk --
 // negated when the tile ends there), first word -1 where the CTA left no piece.  The block of the
 // CTA that holds a tile's first piece owns it; the following pieces are the first records of the
-// next CTAs, up to the one that ends the tile.  blockIdx.y takes every fourth row.
-constexpr int kKcThreads = 128;
+// next CTAs, up to the one that ends the tile.  Four rows per block (blockIdx.y), two warps per row
+// that take every other piece, eight of them in flight (a request over the whole GPU has dozens).
+constexpr int kKcThreads = 256;
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kKcThreads)
 kv4_combine_kernel(const AttnParams p, int ctas) {
     pdl_launch_dependents();
     pdl_wait();
-    __shared__ int s_count;
-    const int c = blockIdx.x, tid = threadIdx.x;
+    __shared__ int s_end;
+    __shared__ float part[4][D + 2];       // what a row's second warp found
+    const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
     const int4 a = p.meta[2 * c], e = p.meta[2 * c + 1];
     int slot = -1;
     int4 me = a;
@@ -735,40 +737,75 @@ kv4_combine_kernel(const AttnParams p, int ctas) {
     const Request r = kv4_request(p, me.x);
     const Units<ROWS> un = kv4_units<ROWS>(p, r);
     const int tile = me.y % un.tiles, kvh = me.y / un.tiles;
-    if (tid == 0) s_count = ctas;
+    if (tid == 0) s_end = ctas;
     __syncthreads();
     // the piece that ends the tile: the first of the following CTAs' first records with a negated end
     for (int j = c + 1 + tid; j < ctas; j += kKcThreads) {
         const int4 m = p.meta[2 * j];
-        const bool end = m.x < 0 || m.w < 0 || m.y != me.y || m.x != me.x;
-        if (end) atomicMin(&s_count, m.w < 0 && m.x == me.x && m.y == me.y ? j + 1 : j);
+        const bool same = m.x == me.x && m.y == me.y;
+        if (!same) atomicMin(&s_end, j);
+        else if (m.w < 0) atomicMin(&s_end, j + 1);
     }
     __syncthreads();
-    const int last = s_count;                                     // pieces: slot, then 2j for c < j < last
+    const int pieces = s_end - c;                                 // slot, then 2j for c < j < s_end
+    const int q = tid >> 6, half = (tid >> 5) & 1;                // row of this block's four, every other piece
+    const int row = 4 * blockIdx.y + q;
     const int rows = min(ROWS, r.nq * p.group - tile * ROWS);
-    const int n = ka_piece<D, ROWS>();
-    constexpr int kPer = D / 4;                                   // threads per row: 4 channels each
-    for (int x = tid; x < (ROWS / 4) * kPer; x += kKcThreads) {
-        const int row = (x / kPer) * 4 + blockIdx.y, d0 = (x % kPer) * 4;
-        if (row >= rows) continue;
-        const float* first = p.part + static_cast<int64_t>(slot) * n;
-        float mm = first[ROWS * D + row];
-        for (int j = c + 1; j < last; ++j) mm = fmaxf(mm, p.part[static_cast<int64_t>(2 * j) * n + ROWS * D + row]);
-        float ll = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int j = c; j < last; ++j) {
-            const float* q = j == c ? first : p.part + static_cast<int64_t>(2 * j) * n;
-            const float f = mm == -INFINITY ? 0.0f : ex2(q[ROWS * D + row] - mm);
-            const float4 v = *reinterpret_cast<const float4*>(q + row * D + d0);
-            ll += f * q[ROWS * D + ROWS + row];
-            o.x += f * v.x; o.y += f * v.y; o.z += f * v.z; o.w += f * v.w;
+    constexpr int n = ka_piece<D, ROWS>();
+    constexpr int kC = D / 32;                                    // channels per lane
+    float mm = -INFINITY, ll = 0.0f, o[kC] = {};
+    if (row < rows) {
+        for (int j0 = half; j0 < pieces; j0 += 16) {
+            float mj[8], lj[8], v[8][kC];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = j0 + 2 * i;
+                const float* src = p.part + static_cast<int64_t>(j == 0 ? slot : 2 * (c + j)) * n;
+                const bool in = j < pieces;
+                mj[i] = in ? src[ROWS * D + row] : -INFINITY;
+                lj[i] = in ? src[ROWS * D + ROWS + row] : 0.0f;
+#pragma unroll
+                for (int k = 0; k < kC; k += 2) {
+                    const float2 x = in ? *reinterpret_cast<const float2*>(src + row * D + kC * lane + k) : make_float2(0.0f, 0.0f);
+                    v[i][k] = x.x;
+                    v[i][k + 1] = x.y;
+                }
+            }
+            float top = mm;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, mj[i]);
+            const float f0 = top == -INFINITY ? 0.0f : ex2(mm - top);
+            mm = top;
+            ll *= f0;
+#pragma unroll
+            for (int k = 0; k < kC; ++k) o[k] *= f0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float f = top == -INFINITY ? 0.0f : ex2(mj[i] - top);
+                ll += f * lj[i];
+#pragma unroll
+                for (int k = 0; k < kC; ++k) o[k] += f * v[i][k];
+            }
         }
-        const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
-        const int64_t at = ka_out_row(p, r, kvh, tile * ROWS + row);
-        *reinterpret_cast<uint2*>(p.out + at * D + d0) =
-            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-        if (d0 == 0 && p.lse) p.lse[at] = ll > 0.0f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+        if (half == 1) {
+#pragma unroll
+            for (int k = 0; k < kC; ++k) part[q][kC * lane + k] = o[k];
+            if (lane == 0) { part[q][D] = mm; part[q][D + 1] = ll; }
+        }
     }
+    __syncthreads();
+    if (row >= rows || half == 1) return;
+    const float m1 = part[q][D], top = fmaxf(mm, m1);
+    const float f0 = top == -INFINITY ? 0.0f : ex2(mm - top), f1 = top == -INFINITY ? 0.0f : ex2(m1 - top);
+    ll = ll * f0 + part[q][D + 1] * f1;
+    const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+    const int64_t at = ka_out_row(p, r, kvh, tile * ROWS + row);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * D + kC * lane);
+#pragma unroll
+    for (int k = 0; k < kC; k += 2)
+        dst[k / 2] = pack_bf16((o[k] * f0 + part[q][kC * lane + k] * f1) * inv,
+                               (o[k + 1] * f0 + part[q][kC * lane + k + 1] * f1) * inv);
+    if (lane == 0 && p.lse) p.lse[at] = ll > 0.0f ? (top + log2f(ll)) * 0.6931471805599453f : -INFINITY;
 }
 
 }  // namespace qat4

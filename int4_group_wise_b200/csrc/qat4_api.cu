@@ -1075,7 +1075,7 @@ static bool kv4_decode_launch(const qat4::AttnParams& p, int64_t chunks, cudaStr
                           qat4::kKaThreads, L::kSmem, stream, qat4::kKaCluster, p);
     const int grid = kKaSms * L::kPerSm;
     return launch_pdl(qat4::kv4_decode_kernel<D, ROWS, false>, dim3(grid), qat4::kKaThreads, L::kSmem, stream, 1, p) &&
-           launch_pdl(qat4::kv4_combine_kernel<D, ROWS>, dim3(grid, 4), qat4::kKcThreads, 0, stream, 1, p, grid);
+           launch_pdl(qat4::kv4_combine_kernel<D, ROWS>, dim3(grid, ROWS / 4), qat4::kKcThreads, 0, stream, 1, p, grid);
 }
 
 template <int D>
