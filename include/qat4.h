@@ -467,8 +467,8 @@ qat4_status qat4_kv4_gather(const qat4_kv4_cache *cache, const int32_t *slots, i
  *            gives zeros.
  *  lse       float32 [N, q_heads] (may be NULL): log of the sum of exp(scale q.k),
  *            -infinity where no key is seen.
- *  workspace device scratch of at least qat4_kv4_attention_workspace_bytes bytes,
- *            16-byte aligned; contents on entry are ignored.  Calls that may
+ *  workspace device scratch of at least qat4_kv4_attention_workspace_bytes bytes
+ *            (may be NULL when that is 0), 16-byte aligned; contents on entry are ignored.  Calls that may
  *            overlap on the GPU (other streams, two captured graphs) need one
  *            each.
  *  Keys and values enter exactly, products are exact, sums and statistics
@@ -479,7 +479,8 @@ qat4_status qat4_kv4_gather(const qat4_kv4_cache *cache, const int32_t *slots, i
  *  all; with scale * q.k overflowing float32 the row is unspecified.
  *  Errors: QAT4_ERR_NULL, _SHAPE, _ALIGN, _WORKSPACE, _CUDA; a bounded wait that
  *  gives up leaves QAT4_ERR_TIMEOUT for qat4_sync_check. */
-size_t qat4_kv4_attention_workspace_bytes(int64_t N, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+size_t qat4_kv4_attention_workspace_bytes(int64_t N, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                          int32_t page_size, int64_t max_blocks);
 qat4_status qat4_kv4_attention(const uint16_t *q, int64_t q_stride, int64_t N, int64_t q_heads,
                                const qat4_kv4_cache *cache, const int32_t *block_table, int64_t table_stride,
                                int64_t max_blocks, const int32_t *seq_lens, const int32_t *cu_q, int64_t B,

@@ -14,6 +14,7 @@ Functions (same names as the C entry points, without the ``qat4_`` prefix):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as ct
 import math
 import os
@@ -60,7 +61,7 @@ EXPORTS = {
     "qat4_kv4_tables": (ct.c_int, [_P, _P, _I64, _P, _I64, _I64, _P, _I64, _I32, _P, _P, _P, _I64, _P, _P]),
     "qat4_kv4_append": (ct.c_int, [_P, _P, _P, ct.c_int, _I64, _I64, _P, _I64, _P]),
     "qat4_kv4_gather": (ct.c_int, [_P, _P, _I64, _P, _P, _P]),
-    "qat4_kv4_attention_workspace_bytes": (_Z, [_I64, _I64, _I64, _I64, _I64]),
+    "qat4_kv4_attention_workspace_bytes": (_Z, [_I64, _I64, _I64, _I64, _I64, _I32, _I64]),
     "qat4_kv4_attention": (ct.c_int, [_P, _I64, _I64, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _F, _I32, _I32, _P, _P,
                                       _P, _Z, _P]),
     "qat4_sync_check": (ct.c_int, [_P]),
@@ -491,10 +492,9 @@ def refine(W, H, alpha, idx, sweeps=1, delta=None, obj=None, workspace=None, str
 
 
 # ------------------------------------------------------------------ 4-bit key/value cache
-class _CacheStruct(ct.Structure):
-    """qat4_kv4_cache of include/qat4.h."""
-    _fields_ = [("k_codes", _P), ("k_scales", _P), ("v_codes", _P), ("v_scales", _P), ("num_pages", _I64),
-                ("page_size", _I32), ("kv_heads", _I32), ("head_dim", _I32)]
+# These calls take a few microseconds on the device, so their accepting path is kept short: one test of all
+# that must hold, and the messages only when it fails.
+_pack_cache = struct.Struct("@PPPPqiii4x").pack       # qat4_kv4_cache of include/qat4.h
 
 
 class KV4Cache(NamedTuple):
@@ -517,82 +517,90 @@ def kv4_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, devi
 
 
 def _arg(t, name, dtype, shape=None):
-    """Pointer of a contiguous CUDA tensor; what _dev refuses is refused by _dev (these calls take a few
-    microseconds on the device, so the accepting path is kept short)."""
+    """Pointer of a contiguous CUDA tensor (what this refuses, _dev names)."""
     if t.is_cuda and t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous():
         return t.data_ptr()
     return _dev(t, name, dtype, shape)
 
 
-def _cache_struct(cache):
+def _cache_arg(cache):
+    """(qat4_kv4_cache as bytes, kv_heads, head_dim) of a KV4Cache or a tuple like it."""
     import torch
     kc, ks, vc, vs = cache
     if not isinstance(kc, torch.Tensor) or kc.dim() != 4:
         raise ValueError("k_codes must be [num_pages, kv_heads, page_size, head_dim / 2]")
     n, h, p, half = codes = kc.shape
     steps = (n, h, p, half // 16)
-    return _CacheStruct(_arg(kc, "k_codes", torch.uint8), _arg(ks, "k_scales", torch.bfloat16, steps),
-                        _arg(vc, "v_codes", torch.uint8, codes), _arg(vs, "v_scales", torch.bfloat16, steps),
-                        n, p, h, 2 * half)
+    u8, bf16 = torch.uint8, torch.bfloat16
+    ptrs = (_arg(kc, "k_codes", u8), _arg(ks, "k_scales", bf16, steps), _arg(vc, "v_codes", u8, codes),
+            _arg(vs, "v_scales", bf16, steps))
+    if p >= 1 << 31 or h >= 1 << 31 or half >= 1 << 30:
+        raise ValueError(f"cache of shape {tuple(codes)}")
+    return _pack_cache(*ptrs, n, p, h, 2 * half), h, 2 * half
 
 
-def _same_device(first, *others):
-    """Index of the CUDA device that all tensors share; the call is made with it current."""
-    d = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != d:
-            raise ValueError(f"all tensors must be on one device, got {first.device} and {t.device}")
-    return d
-
-
-class _on:
+class _On:
     """Makes device `d` current for a call, and `stream` (when given) the current stream, so that outputs and
-    workspaces allocated inside belong to the stream that uses them; gives the stream's handle."""
-    __slots__ = ("d", "stream", "guards")
+    workspaces allocated inside belong to the stream that uses them."""
 
     def __init__(self, d, stream):
-        self.d, self.stream, self.guards = d, stream, ()
+        import torch
+        if stream is not None and stream.device.index != d:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{d}")
+        self.guards = (torch.cuda.device(d),) if stream is None else (torch.cuda.device(d), torch.cuda.stream(stream))
 
     def __enter__(self):
-        import torch
-        s = self.stream
-        if s is None and torch._C._cuda_getDevice() == self.d:
-            return torch._C._cuda_getCurrentRawStream(self.d)
-        if s is not None and s.device.index != self.d:
-            raise ValueError(f"the stream is on {s.device}, the tensors on cuda:{self.d}")
-        self.guards = (torch.cuda.device(self.d),) if s is None else (torch.cuda.device(self.d), torch.cuda.stream(s))
         for g in self.guards:
             g.__enter__()
-        return torch.cuda.current_stream(self.d).cuda_stream
 
     def __exit__(self, *exc):
         for g in reversed(self.guards):
             g.__exit__(*exc)
 
 
+_here = contextlib.nullcontext()
+
+
+def _on(stream, first, *others):
+    """(index of the device that all tensors share, context of the call)."""
+    import torch
+    d = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != d:
+            raise ValueError(f"all tensors must be on one device, got {first.device} and {t.device}")
+    return d, (_here if stream is None and torch._C._cuda_getDevice() == d else _On(d, stream))
+
+
+def _handle(d):
+    import torch
+    return torch._C._cuda_getCurrentRawStream(d)
+
+
 def _rows3(t, name, heads, dim, dtypes):
-    """[n, heads, dim] whose rows may be strided (columns of a stacked projection)."""
+    """Pointer and row stride of [n, heads, dim] whose rows may be strided (columns of a stacked projection)."""
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must be [n, {heads}, {dim}], got {tuple(t.shape)}")
-    s = t.stride()
-    if t.numel() > 0 and ((dim > 1 and s[2] != 1) or (heads > 1 and s[1] != dim)):
-        raise ValueError(f"{name} must have contiguous heads and channels (strides [*, {dim}, 1]), got {s}")
-    return t.data_ptr(), (s[0] if t.shape[0] > 1 else heads * dim)
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [n, {heads}, {dim}], got {tuple(shape)}")
+    row, head, one = t.stride()
+    if shape[0] > 0 and ((dim > 1 and one != 1) or (heads > 1 and head != dim)):
+        raise ValueError(f"{name} must have contiguous heads and channels (strides [*, {dim}, 1]), got {t.stride()}")
+    return t.data_ptr(), (row if shape[0] > 1 else heads * dim)
 
 
 def _table(t):
-    """A block table int32 [B, max_blocks] with contiguous rows (row stride of its own)."""
+    """Pointer, row stride, rows and columns of a block table int32 [B, max_blocks] with contiguous rows."""
     import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.int32:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not torch.int32:
         raise TypeError("block_table must be an int32 CUDA tensor")
     if t.dim() != 2 or t.shape[0] < 1 or t.shape[1] < 1 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError("block_table must be [B, max_blocks] with contiguous rows")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    B, n = t.shape
+    return t.data_ptr(), (t.stride(0) if B > 1 else n), B, n
 
 
 def kv4_tables(lengths, new_lengths, block_table, free_pages, page_size, num_slots, seq_lens=None, cu_new=None,
@@ -604,28 +612,28 @@ def kv4_tables(lengths, new_lengths, block_table, free_pages, page_size, num_slo
     kv4_append skips, so a padded batch can be captured in a graph).  taken > F means that the free list
     was too short: the tokens without a page have slot -1."""
     import torch
-    L = lib()
-    lp = _arg(lengths, "lengths", torch.int32)
-    if lengths.dim() != 1 or lengths.shape[0] < 1:
-        raise ValueError("lengths must be [B] with B >= 1")
-    B = lengths.shape[0]
-    np_ = _arg(new_lengths, "new_lengths", torch.int32, (B,))
-    tp, ts = _table(block_table)
-    if block_table.shape[0] != B:
-        raise ValueError(f"block_table must have {B} rows, got {block_table.shape[0]}")
-    fp = _arg(free_pages, "free_pages", torch.int32)
-    dev = _same_device(lengths, new_lengths, block_table, free_pages, seq_lens, cu_new, slots, taken)
+    i32 = torch.int32
+    tp, ts, B, blocks = _table(block_table)
+    lp, np_ = _arg(lengths, "lengths", i32, (B,)), _arg(new_lengths, "new_lengths", i32, (B,))
+    fp = _arg(free_pages, "free_pages", i32)
     num_slots, page_size = int(num_slots), int(page_size)
     if num_slots < 0 or num_slots >= 1 << 31 or page_size not in (16, 32, 64, 128):
         raise ValueError("num_slots must be in [0, 2^31), page_size 16, 32, 64 or 128")
-    with _on(dev, stream) as handle:
-        seq_lens = _out(seq_lens, "seq_lens", (B,), torch.int32, lengths)
-        cu_new = _out(cu_new, "cu_new", (B + 1,), torch.int32, lengths)
-        slots = _out(slots, "slots", (num_slots,), torch.int32, lengths)
-        taken = _out(taken, "taken", (), torch.int32, lengths)
-        _check(L.qat4_kv4_tables(lp, np_, B, tp, ts, block_table.shape[1], fp, free_pages.numel(), page_size,
-                                 seq_lens.data_ptr(), cu_new.data_ptr(), slots.data_ptr(), num_slots,
-                                 taken.data_ptr(), handle), "qat4_kv4_tables")
+    d, place = _on(stream, lengths, new_lengths, block_table, free_pages, seq_lens, cu_new, slots, taken)
+    with place:
+        if seq_lens is None and cu_new is None and slots is None and taken is None and num_slots <= 1 << 16:
+            room = lengths.new_empty((num_slots + 2 * B + 2,))      # the outputs of a step in one allocation
+            slots, cu_new, seq_lens, _ = room.split_with_sizes((num_slots, B + 1, B, 1))
+            taken = room.as_strided((), (), num_slots + 2 * B + 1)
+        else:
+            seq_lens = _out(seq_lens, "seq_lens", (B,), i32, lengths)
+            cu_new = _out(cu_new, "cu_new", (B + 1,), i32, lengths)
+            slots = _out(slots, "slots", (num_slots,), i32, lengths)
+            taken = _out(taken, "taken", (), i32, lengths)
+        st = lib().qat4_kv4_tables(lp, np_, B, tp, ts, blocks, fp, free_pages.numel(), page_size, seq_lens.data_ptr(),
+                                   cu_new.data_ptr(), slots.data_ptr(), num_slots, taken.data_ptr(), _handle(d))
+        if st:
+            _check(st, "qat4_kv4_tables")
     return seq_lens, cu_new, slots, taken
 
 
@@ -633,39 +641,45 @@ def kv4_append(cache, k, v, slots, stream=None):
     """Quantizes k and v (bfloat16 or float32 [n, kv_heads, head_dim], rows may be strided) and writes
     token i to slot slots[i] (int32 [n]) of the cache; negative slots are skipped."""
     import torch
-    L = lib()
-    c = _cache_struct(cache)
-    kinds = (torch.bfloat16, torch.float32)
-    kp, ks = _rows3(k, "k", c.kv_heads, c.head_dim, kinds)
-    vp, vs = _rows3(v, "v", c.kv_heads, c.head_dim, (k.dtype,))
-    if v.shape[0] != k.shape[0]:
+    c, heads, dim = _cache_arg(cache)
+    kp, ks = _rows3(k, "k", heads, dim, (torch.bfloat16, torch.float32))
+    vp, vs = _rows3(v, "v", heads, dim, (k.dtype,))
+    n = k.shape[0]
+    if v.shape[0] != n:
         raise ValueError("k and v must have the same number of tokens")
-    sp = _arg(slots, "slots", torch.int32, (k.shape[0],))
-    with _on(_same_device(k, v, slots, *cache), stream) as handle:
-        _check(L.qat4_kv4_append(ct.byref(c), kp, vp, _gdtype(k), ks, vs, sp, k.shape[0], handle),
-               "qat4_kv4_append")
+    sp = _arg(slots, "slots", torch.int32, (n,))
+    d, place = _on(stream, k, v, slots, *cache)
+    with place:
+        st = lib().qat4_kv4_append(c, kp, vp, _gdtype(k), ks, vs, sp, n, _handle(d))
+        if st:
+            _check(st, "qat4_kv4_append")
 
 
 def kv4_gather(cache, slots, k=None, v=None, stream=None):
     """The values of the tokens in slots (int32 [n]) as bfloat16 (k, v), each [n, kv_heads, head_dim];
     zeros for negative slots."""
     import torch
-    L = lib()
-    c = _cache_struct(cache)
+    c, heads, dim = _cache_arg(cache)
     sp = _arg(slots, "slots", torch.int32)
     if slots.dim() != 1:
         raise ValueError("slots must be [n]")
-    shape = (slots.shape[0], c.kv_heads, c.head_dim)
-    with _on(_same_device(slots, k, v, *cache), stream) as handle:
-        k = _out(k, "k", shape, torch.bfloat16, slots)
-        v = _out(v, "v", shape, torch.bfloat16, slots)
-        _check(L.qat4_kv4_gather(ct.byref(c), sp, shape[0], k.data_ptr(), v.data_ptr(), handle),
-               "qat4_kv4_gather")
+    n = slots.shape[0]
+    shape = (n, heads, dim)
+    d, place = _on(stream, slots, k, v, *cache)
+    with place:
+        k = cache[1].new_empty(shape) if k is None else _out(k, "k", shape, torch.bfloat16, slots)
+        v = cache[1].new_empty(shape) if v is None else _out(v, "v", shape, torch.bfloat16, slots)
+        st = lib().qat4_kv4_gather(c, sp, n, k.data_ptr(), v.data_ptr(), _handle(d))
+        if st:
+            _check(st, "qat4_kv4_gather")
     return k, v
 
 
-def kv4_attention_workspace_bytes(N: int, B: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
-    return int(lib().qat4_kv4_attention_workspace_bytes(int(N), int(B), int(q_heads), int(kv_heads), int(head_dim)))
+def kv4_attention_workspace_bytes(N: int, B: int, q_heads: int, kv_heads: int, head_dim: int, page_size: int,
+                                  max_blocks: int) -> int:
+    """Bytes of workspace of a kv4_attention call (0: none is needed)."""
+    return int(lib().qat4_kv4_attention_workspace_bytes(int(N), int(B), int(q_heads), int(kv_heads), int(head_dim),
+                                                        int(page_size), int(max_blocks)))
 
 
 def kv4_attention(q, cache, block_table, seq_lens, cu_q, scale=None, causal=True, window=0, out=None, lse=None,
@@ -678,30 +692,33 @@ def kv4_attention(q, cache, block_table, seq_lens, cu_q, scale=None, causal=True
     cu_q[B] are not written."""
     import torch
     L = lib()
-    c = _cache_struct(cache)
+    c, heads, dim = _cache_arg(cache)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be [N, q_heads, head_dim]")
-    N, Hq = q.shape[0], q.shape[1]
-    if Hq < 1 or Hq % c.kv_heads != 0:
-        raise ValueError(f"q_heads ({Hq}) must be a multiple of kv_heads ({c.kv_heads})")
-    qp, qs = _rows3(q, "q", Hq, c.head_dim, (torch.bfloat16,))
-    tp, ts = _table(block_table)
-    B = block_table.shape[0]
-    lp = _arg(seq_lens, "seq_lens", torch.int32, (B,))
-    cp = _arg(cu_q, "cu_q", torch.int32, (B + 1,))
-    dev = _same_device(q, block_table, seq_lens, cu_q, out, lse, workspace, *cache)
-    scale = 1.0 / math.sqrt(c.head_dim) if scale is None else float(scale)
+    N, Hq, _ = shape = q.shape
+    if Hq < 1 or Hq % heads != 0:
+        raise ValueError(f"q_heads ({Hq}) must be a multiple of kv_heads ({heads})")
+    qp, qs = _rows3(q, "q", Hq, dim, (torch.bfloat16,))
+    tp, ts, B, blocks = _table(block_table)
+    lp, cp = _arg(seq_lens, "seq_lens", torch.int32, (B,)), _arg(cu_q, "cu_q", torch.int32, (B + 1,))
+    scale = 1.0 / math.sqrt(dim) if scale is None else float(scale)
     window = max(-1, min(int(window), 0x7fffffff))
-    with _on(dev, stream) as handle:
-        out = _out(out, "out", (N, Hq, c.head_dim), torch.bfloat16, q)
+    d, place = _on(stream, q, block_table, seq_lens, cu_q, out, lse, workspace, *cache)
+    with place:
+        if out is None:
+            out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(shape)
+        else:
+            _dev(out, "out", torch.bfloat16, shape)
         if workspace is None:
-            need = L.qat4_kv4_attention_workspace_bytes(N, B, Hq, c.kv_heads, c.head_dim)
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        _check(L.qat4_kv4_attention(qp, qs, N, Hq, ct.byref(c), tp, ts, block_table.shape[1], lp, cp, B, scale,
-                                    int(bool(causal)), window, out.data_ptr(),
-                                    _arg(lse, "lse", torch.float32, (N, Hq)) if lse is not None else None,
-                                    _arg(workspace, "workspace", torch.uint8), workspace.numel(), handle),
-               "qat4_kv4_attention")
+            need = L.qat4_kv4_attention_workspace_bytes(N, B, Hq, heads, dim, cache[0].shape[2], blocks)
+            if need:
+                workspace = cache[0].new_empty((need,))
+        wp, wn = (_arg(workspace, "workspace", torch.uint8), workspace.numel()) if workspace is not None else (None, 0)
+        st = L.qat4_kv4_attention(qp, qs, N, Hq, c, tp, ts, blocks, lp, cp, B, scale, 1 if causal else 0, window,
+                                  out.data_ptr(), None if lse is None else _arg(lse, "lse", torch.float32, (N, Hq)),
+                                  wp, wn, _handle(d))
+        if st:
+            _check(st, "qat4_kv4_attention")
     return out
 
 

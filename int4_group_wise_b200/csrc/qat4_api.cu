@@ -1053,25 +1053,40 @@ static size_t kv4_decode_bytes(int64_t D) {
     return static_cast<size_t>(kKaGrid) * 2 * (16 + 16 * (static_cast<size_t>(D) + 2) * 4);
 }
 
-extern "C" size_t qat4_kv4_attention_workspace_bytes(int64_t N, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
-    if (N < 0 || B < 1 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128) ||
-        N > ((int64_t(1) << 31) - 1) / q_heads)
+// Rows of the decode kernel's tiles: as tall as the average request's.
+static int kv4_tile_rows(int64_t rows, int64_t B) { return rows <= 4 * B ? 4 : rows <= 8 * B ? 8 : 16; }
+
+// Clusters of the one-launch form of the decode kernel (upper bound of the row tiles over all kv heads), or 0
+// where the batch fills the GPU, or a request may be longer than four chunks for each CTA of a cluster (one
+// request of 999 tokens: 6.6 us against 11.2 with the grid-wide split and its second launch; past that length
+// the split over all SMs wins).
+static int64_t kv4_clusters(int64_t N, int64_t B, int64_t group, int64_t kv_heads, int64_t page, int64_t max_blocks) {
+    const int64_t rows = N * group, chunk = qat4::kKaChunk;
+    if ((max_blocks * page + chunk - 1) / chunk > 4 * qat4::kKaCluster) return 0;
+    const int64_t tiles = (rows / kv4_tile_rows(rows, B) + std::min(B, rows)) * kv_heads;
+    return tiles * qat4::kKaCluster <= 2 * kKaSms ? tiles : 0;
+}
+
+extern "C" size_t qat4_kv4_attention_workspace_bytes(int64_t N, int64_t B, int64_t q_heads, int64_t kv_heads,
+                                                     int64_t head_dim, int32_t page_size, int64_t max_blocks) {
+    const int64_t top = (int64_t(1) << 31) - 1;
+    if (N < 0 || B < 1 || B > 65536 || q_heads < 1 || q_heads > 65536 || kv_heads < 1 || q_heads % kv_heads != 0 ||
+        (head_dim != 64 && head_dim != 128) || N > top / q_heads || page_size < 1 || max_blocks < 1 || max_blocks > top)
         return 0;
-    const Kv4Plan pl = kv4_plan(N, B, q_heads / kv_heads, kv_heads);
-    size_t bytes = kv4_decode_bytes(head_dim);
+    const int64_t group = q_heads / kv_heads;
+    const Kv4Plan pl = kv4_plan(N, B, group, kv_heads);
+    size_t bytes = 0;
+    if (pl.decode && kv4_clusters(N, B, group, kv_heads, page_size, max_blocks) == 0) bytes += kv4_decode_bytes(head_dim);
     if (pl.splits > 1)
         bytes += (static_cast<size_t>(pl.splits) * N * q_heads * (head_dim + 2) * 4 + 255) & ~size_t(255);
     return bytes;
 }
 
-// tiles: upper bound of the row tiles over all kv heads; chunks: most chunks of a request.
 template <int D, int ROWS>
-static bool kv4_decode_launch(const qat4::AttnParams& p, int64_t chunks, cudaStream_t stream) {
+static bool kv4_decode_launch(const qat4::AttnParams& p, int64_t clusters, cudaStream_t stream) {
     using L = qat4::KaLayout<D, ROWS>;
-    const int64_t rows = static_cast<int64_t>(p.N) * p.group;
-    const int64_t tiles = (rows / ROWS + std::min<int64_t>(p.B, rows)) * p.c.heads;
-    if (tiles * qat4::kKaCluster <= kKaGrid && chunks <= 4 * qat4::kKaCluster)
-        return launch_pdl(qat4::kv4_decode_kernel<D, ROWS, true>, dim3(static_cast<unsigned>(tiles * qat4::kKaCluster)),
+    if (clusters > 0)
+        return launch_pdl(qat4::kv4_decode_kernel<D, ROWS, true>, dim3(static_cast<unsigned>(clusters * qat4::kKaCluster)),
                           qat4::kKaThreads, L::kSmem, stream, qat4::kKaCluster, p);
     const int grid = kKaSms * L::kPerSm;
     return launch_pdl(qat4::kv4_decode_kernel<D, ROWS, false>, dim3(grid), qat4::kKaThreads, L::kSmem, stream, 1, p) &&
@@ -1079,11 +1094,11 @@ static bool kv4_decode_launch(const qat4::AttnParams& p, int64_t chunks, cudaStr
 }
 
 template <int D>
-static bool kv4_decode_rows(const qat4::AttnParams& p, int64_t chunks, cudaStream_t stream) {
-    const int64_t rows = static_cast<int64_t>(p.N) * p.group;      // tiles as tall as the average request's rows
-    return rows <= 4 * static_cast<int64_t>(p.B) ? kv4_decode_launch<D, 4>(p, chunks, stream)
-         : rows <= 8 * static_cast<int64_t>(p.B) ? kv4_decode_launch<D, 8>(p, chunks, stream)
-                                                 : kv4_decode_launch<D, 16>(p, chunks, stream);
+static bool kv4_decode_rows(const qat4::AttnParams& p, int64_t clusters, cudaStream_t stream) {
+    const int rows = kv4_tile_rows(static_cast<int64_t>(p.N) * p.group, p.B);
+    return rows == 4 ? kv4_decode_launch<D, 4>(p, clusters, stream)
+         : rows == 8 ? kv4_decode_launch<D, 8>(p, clusters, stream)
+                     : kv4_decode_launch<D, 16>(p, clusters, stream);
 }
 
 template <int D>
@@ -1104,7 +1119,7 @@ qat4_status qat4_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t N, i
                                void* workspace, size_t workspace_bytes, cudaStream_t stream) {
     const qat4_status st = kv4_cache_check(cache);
     if (st != QAT4_OK) return st;
-    if (!block_table || !seq_lens || !cu_q || (N != 0 && (!q || !out)) || !workspace) return QAT4_ERR_NULL;
+    if (!block_table || !seq_lens || !cu_q || (N != 0 && (!q || !out))) return QAT4_ERR_NULL;
     const int64_t top = (int64_t(1) << 31) - 1, D = cache->head_dim, H = cache->kv_heads;
     if (N < 0 || B < 1 || B > 65536 || q_heads < 1 || q_heads % H != 0 || q_heads / H > 64 || q_heads > 65536 ||
         N > top / q_heads || N * q_heads / H / qat4::kKpRows + B > top / (16 * H) || q_stride < q_heads * D || q_stride > top || max_blocks < 1 || max_blocks > top ||
@@ -1115,8 +1130,10 @@ qat4_status qat4_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t N, i
     if (!aligned16(q) || q_stride % 8 != 0 || !aligned16(out) || !aligned16(workspace) || !aligned4(block_table) ||
         !aligned4(seq_lens) || !aligned4(cu_q) || !aligned4(lse))
         return QAT4_ERR_ALIGN;
-    if (workspace_bytes < qat4_kv4_attention_workspace_bytes(N, B, q_heads, H, D)) return QAT4_ERR_WORKSPACE;
     if (N == 0) return QAT4_OK;
+    if (workspace_bytes < qat4_kv4_attention_workspace_bytes(N, B, q_heads, H, D, cache->page_size, max_blocks))
+        return QAT4_ERR_WORKSPACE;
+    if (!workspace && workspace_bytes > 0) return QAT4_ERR_NULL;
     int dev = 0;
     DeviceInfo* info = nullptr;
     if (!device_info(&dev, &info) || !kv4_attrs(info)) return QAT4_ERR_CUDA;
@@ -1143,19 +1160,20 @@ qat4_status qat4_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t N, i
     // generous bound of a wait: 10 s (a CTA waits for one unit's copies or one block's products, microseconds)
     p.limit_ns = 10000000000ull;
     const Kv4Plan pl = kv4_plan(N, B, p.group, H);
+    const int64_t clusters = pl.decode ? kv4_clusters(N, B, p.group, H, cache->page_size, max_blocks) : 0;
     bool ok = true;
     if (pl.decode) {
         p.rows_lo = pl.lo_decode;
         p.rows_hi = pl.hi_decode;
-        const int64_t chunks = (max_blocks * cache->page_size + qat4::kKaChunk - 1) / qat4::kKaChunk;
-        ok = D == 64 ? kv4_decode_rows<64>(p, chunks, stream) : kv4_decode_rows<128>(p, chunks, stream);
+        ok = D == 64 ? kv4_decode_rows<64>(p, clusters, stream) : kv4_decode_rows<128>(p, clusters, stream);
     }
     if (ok && pl.prefill) {
         qat4::PrefillParams pp;
         p.rows_lo = pl.lo_prefill;
         p.rows_hi = 0x7fffffff;
         pp.a = p;
-        pp.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kv4_decode_bytes(D));
+        pp.part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                           (pl.decode && clusters == 0 ? kv4_decode_bytes(D) : 0));
         // a part holds at least four blocks of keys of the longest request that the table can name
         pp.splits = static_cast<int>(std::max<int64_t>(
             1, std::min<int64_t>(pl.splits, max_blocks * cache->page_size / (4 * qat4::kKpBlock))));

@@ -533,8 +533,9 @@ def test_refusals_of_the_binding():
         with pytest.raises(q4.Qat4Error) as e:
             call(**kw)
         assert e.value.status == 2
+    wide = torch.zeros((2, 900), dtype=I32, device="cuda")
     with pytest.raises(q4.Qat4Error) as e:
-        call(workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+        call(block_table=wide, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     assert e.value.status == 5
     with pytest.raises(q4.Qat4Error) as e:               # rows of 20 bytes past a 16-byte boundary
         call(q=torch.zeros(2 * 260, dtype=torch.bfloat16, device="cuda").as_strided((2, 4, 64), (260, 64, 1)))

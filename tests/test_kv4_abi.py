@@ -13,10 +13,16 @@ import kv4_ref as ref
 A, MIS4, MIS1 = 0x10000, 0x20004, 0x20001
 
 
+class _Cache(ct.Structure):
+    """qat4_kv4_cache of include/qat4.h."""
+    _fields_ = ([(n, ct.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales")] + [("num_pages", ct.c_int64)] +
+                [(n, ct.c_int32) for n in ("page_size", "kv_heads", "head_dim")])
+
+
 def _cache(**kw):
     d = dict(k_codes=A, k_scales=A, v_codes=A, v_scales=A, num_pages=10, page_size=16, kv_heads=2, head_dim=64)
     d.update(kw)
-    return ct.byref(q4._CacheStruct(*(d[n] for n, _ in q4._CacheStruct._fields_)))
+    return _Cache(*d.values())
 
 
 BAD_CACHES = [(dict(k_codes=None), 1), (dict(v_scales=None), 1), (dict(page_size=8), 2), (dict(page_size=48), 2),
@@ -26,7 +32,7 @@ BAD_CACHES = [(dict(k_codes=None), 1), (dict(v_scales=None), 1), (dict(page_size
 
 @pytest.mark.parametrize("kw,code", BAD_CACHES)
 def test_bad_caches(kw, code):
-    L, c = q4.lib(), _cache(**kw)
+    L, c = q4.lib(), ct.byref(_cache(**kw))
     assert L.qat4_kv4_append(c, A, A, 1, 128, 128, A, 4, None) == code
     assert L.qat4_kv4_gather(c, A, 4, A, A, None) == code
     assert L.qat4_kv4_attention(A, 256, 4, 4, c, A, 8, 8, A, A, 2, 0.1, 1, 0, A, None, A, 1 << 30, None) == code
@@ -34,7 +40,7 @@ def test_bad_caches(kw, code):
 
 
 def test_append_and_gather_validation():
-    L, c = q4.lib(), _cache()
+    L, c = q4.lib(), ct.byref(_cache())
     f = L.qat4_kv4_append
     assert f(c, None, A, 1, 128, 128, A, 4, None) == 1
     assert f(c, A, A, 1, 128, 128, None, 4, None) == 1
@@ -69,26 +75,33 @@ def test_tables_validation(kw, code):
 
 
 def test_attention_validation():
-    L, c = q4.lib(), _cache()
-    need = q4.kv4_attention_workspace_bytes(4, 2, 4, 2, 64)
+    L, c = q4.lib(), ct.byref(_cache())
+    assert q4.kv4_attention_workspace_bytes(4, 2, 4, 2, 64, 16, 8) == 0      # one launch of clusters: none
+    need = q4.kv4_attention_workspace_bytes(4, 2, 4, 2, 64, 16, 800)
     assert need > 0
-    base = dict(q=A, qs=256, N=4, Hq=4, c=c, t=A, ts=8, mb=8, lens=A, cu=A, B=2, scale=0.1, causal=1, window=0, out=A,
+    base = dict(q=A, qs=256, N=4, Hq=4, c=c, t=A, ts=800, mb=800, lens=A, cu=A, B=2, scale=0.1, causal=1, window=0, out=A,
                 lse=None, ws=A, wb=need)
 
     def f(**kw):
         return L.qat4_kv4_attention(*{**base, **kw}.values(), None)
-    for kw in (dict(q=None), dict(t=None), dict(lens=None), dict(cu=None), dict(out=None), dict(ws=None)):
+    for kw in (dict(q=None), dict(t=None), dict(lens=None), dict(cu=None), dict(out=None), dict(ws=None, wb=need)):
         assert f(**kw) == 1, kw
     for kw in (dict(N=-1), dict(B=0), dict(B=65537), dict(Hq=5), dict(Hq=0), dict(Hq=130, qs=130 * 64), dict(qs=248),
-               dict(mb=0), dict(ts=7), dict(scale=0.0), dict(scale=-0.5), dict(scale=math.nan), dict(scale=math.inf),
+               dict(mb=0), dict(ts=799), dict(scale=0.0), dict(scale=-0.5), dict(scale=math.nan), dict(scale=math.inf),
                dict(scale=3e38), dict(causal=2), dict(window=-1), dict(window=3, causal=0), dict(N=1 << 30)):
         assert f(**kw) == 2, kw
     for kw in (dict(q=MIS4), dict(qs=260), dict(out=MIS4), dict(ws=MIS4), dict(t=MIS1), dict(lse=MIS1), dict(cu=MIS1)):
         assert f(**kw) == 3, kw
     assert f(wb=need - 1) == 5
     assert f(N=0, q=None, out=None) == 0                      # no query: nothing to do
-    for bad in ((-1, 2, 4, 2, 64), (4, 0, 4, 2, 64), (4, 2, 5, 2, 64), (4, 2, 4, 2, 80)):
+    for bad in ((-1, 2, 4, 2, 64, 16, 800), (4, 0, 4, 2, 64, 16, 800), (4, 2, 5, 2, 64, 16, 800), (4, 2, 4, 2, 80, 16, 800),
+                (4, 2, 4, 2, 64, 16, 0)):
         assert q4.kv4_attention_workspace_bytes(*bad) == 0
+
+
+def test_binding_packs_the_c_struct():
+    c = _cache()
+    assert q4._pack_cache(*(getattr(c, n) for n, _ in c._fields_)) == bytes(c)
 
 
 def test_binding_refuses_host_tensors_and_bad_caches():
