@@ -339,7 +339,7 @@ kv4_decode_kernel(const AttnParams p) {
             ahead.next(p, u + 1 < u1);
             const int id_next = u + 1 < u1 ? entry(ahead) : -1;
             int ok = 1;
-            if (lane == 0) ok = mbar_wait(&empty_bar[s], ph ^ 1u, abort, p.limit_ns) ? 1 : 0;
+            if (lane == 0) ok = kv4_wait(&empty_bar[s], ph ^ 1u, abort, p.limit_ns) ? 1 : 0;
             if (!__shfl_sync(0xffffffffu, ok, 0)) break;
             if (id >= p.c.pages) id = -1;
             const int t0 = at.t0(), pt = t0 + pi * page;
@@ -427,7 +427,7 @@ kv4_decode_kernel(const AttnParams p) {
                 seg_c0 = at.ch;
                 fresh = false;
             }
-            dead = dead || !mbar_wait(&full_bar[s], ph, abort, p.limit_ns);
+            dead = dead || !kv4_wait(&full_bar[s], ph, abort, p.limit_ns);
             dead = __any_sync(0xffffffffu, dead);
             if (!dead) {
                 const uint32_t sb = ring + s * L::kStage;

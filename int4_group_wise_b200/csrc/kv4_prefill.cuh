@@ -6,29 +6,31 @@
 // bf16 rate and 1024 of the SM's 16 exponentials per clock, so both pipes have
 // to run all the time.
 //
-// One CTA (one per SM) owns 256 query rows (token * group + head, as in the
-// decode kernel) of one kv head as two tiles of M = 128, and walks its keys in
-// blocks of 128:
-//   warps 0-3, 4-7  softmax of tile 0 / 1, one thread per row: S from TMEM, row
-//                   maximum, exp2, P back to TMEM as bf16 (the A operand of the
-//                   second product), O rescaled in TMEM only when the maximum
-//                   grows by more than 2^8
+// A work item is 256 query rows (token * group + head, as in the decode kernel)
+// of one kv head, as two tiles of M = 128, over the keys that they see, in
+// blocks of 128.  A CTA stays on its SM and takes item after item: the grid has
+// one CTA per item, the last (longest) first, and a running CTA takes over the
+// next one that has not started (clusterlaunchcontrol), so the end of one item
+// overlaps the beginning of the next:
+//   warps 0-3, 4-7  softmax of tile 0 / 1, one thread per row, 64 keys at a time:
+//                   S from TMEM, exp2, P back to TMEM as bf16 over its S (the A
+//                   operand of the second product); O is rescaled in TMEM only
+//                   when the reference moves
 //   warps 8-11      decode the block's codes (one thread per token) into bf16
 //                   operands in shared memory, double buffered
-//   warp 12         issues the MMAs: S = Q K^T (both K-major) and O += P V (V as
-//                   stored, MN-major); tile 0's products run while tile 1's
-//                   softmax does, and the other way round
+//   warps 12, 13    issue tile 0's / 1's MMAs: S = Q K^T (both K-major, N = 64) into
+//                   two TMEM buffers, two steps ahead of the softmax, and
+//                   O += P V (V as stored, MN-major)
+//   warp 14         takes the next item
 // The codes are decoded in the order (0, 4, 1, 5, 2, 6, 3, 7) of each 8
 // channels, which needs no reordering of the packed words: Q is staged in the
 // same order, and O's columns are put back in order on the way out.
 //
-// TMEM: S of both tiles [0, 256), O [256, 256 + 2 D); P overlays its S at
-// D = 128 (the next S of a tile is issued after the product that reads P, in
-// order and of the same shape) and has columns of its own at D = 64.
+// TMEM: S of tile x, buffer u in columns [128 x + 64 u, + 64), O of tile x in
+// [256 + D x, + D).
 //
-// With few row tiles the keys of each are cut into `splits` equal parts (grid
-// y), which leave (maximum, sum, unnormalised O) in the workspace for
-// kv4_join_kernel.
+// With few row tiles the keys of each are cut into `splits` equal parts, which
+// leave (maximum, sum, unnormalised O) in the workspace for kv4_join_kernel.
 #pragma once
 
 #include "hessian.cuh"
@@ -37,8 +39,8 @@
 namespace qat4 {
 
 constexpr int kKpThreads = 512;                    // 2 softmax warpgroups, 1 decoding, 1 issuing
-constexpr int kKpRegsSoftmax = 184, kKpRegsDecode = 96, kKpRegsIssue = 40;   // per thread; their sum over the four
-                                                   // warpgroups is below the 128 per thread of the launch
+constexpr int kKpRegsSoftmax = 176, kKpRegsDecode = 96, kKpRegsIssue = 64;   // per thread; their sum over the four
+                                                   // warpgroups is the 128 per thread of the launch
 constexpr int kKpRows = 256;
 constexpr int kKpBlock = 128;                      // keys per block
 constexpr uint32_t kKpHalf = 128 * 128;            // 128 rows x 64 channels bf16: 16 KB
@@ -49,8 +51,6 @@ struct KpLayout {
     static constexpr uint32_t kQ = 0, kK = 2 * kTile, kV = 4 * kTile;
     static constexpr size_t kSmem = 6 * kTile + 1024;
     static constexpr uint32_t kO = 256;                            // TMEM columns
-    static constexpr uint32_t kP = D == 128 ? 0 : 256 + 2 * D;
-    static constexpr uint32_t kPStride = D == 128 ? 128 : 64;
 };
 
 struct PrefillParams {
@@ -78,6 +78,11 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
            "r"(r[14]), "r"(r[15])
         : "memory");
 }
+__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return d;
+}
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;"
@@ -90,6 +95,17 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     asm("add.rn.f32x2 %0, %1, %2;"
         : "=l"(reinterpret_cast<uint64_t&>(d)) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
     return d;
+}
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
 }
 
 // Row tiles of a request in this kernel.
@@ -143,89 +159,102 @@ __device__ __forceinline__ void kp_decode(const KpRow<D>& r, uint32_t base, int 
     }
 }
 
+// A work item as its roles need it.
+struct KpItem {
+    int state;                // 1: work, -1: no more
+    int b, kvh, row0, rows;   // request, kv head, first row and rows of the request
+    int q0, len, first, lo;   // of the request (see Request)
+    int t_first, n, split;    // first key, blocks of 128 keys
+};
+
+// Item `idx` of the grid, found by a converged warp: split, kv head, and the rank of its row tile, the
+// last (longest) tile of a request first.  Up to 32 requests are taken from the longest to the
+// shortest, so that short items even out the end; more are taken as they come.  False where there are
+// fewer tiles.
+__device__ __forceinline__ bool kp_locate(const PrefillParams& pp, int idx, int lane, KpItem& it) {
+    const AttnParams& p = pp.a;
+    it.split = idx % pp.splits;
+    const int hr = idx / pp.splits;
+    it.kvh = hr % p.c.heads;
+    int rank = hr / p.c.heads;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane;
+        Request r = {0, 0, 0, 0, 0};
+        if (b < p.B) r = kv4_request(p, b);
+        const int n = b < p.B ? kp_tiles(p, r) : 0;
+        int before = 0, all = 0;                                   // tiles of the requests that come first, of all
+        for (int j = 0; j < 32 && b0 + j < p.B; ++j) {
+            const int nj = __shfl_sync(0xffffffffu, n, j), lj = __shfl_sync(0xffffffffu, r.len, j);
+            if (p.B <= 32 ? lj > r.len || (lj == r.len && j < lane) : j < lane) before += nj;
+            all += nj;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, rank >= before && rank < before + n);
+        if (hit == 0) {
+            rank -= all;
+            continue;
+        }
+        const int src = __ffs(hit) - 1;
+        const int tile = n - 1 - (rank - before);                  // right in lane src
+        it.state = 1;
+        it.b = b0 + src;
+        it.row0 = __shfl_sync(0xffffffffu, tile, src) * kKpRows;
+        it.q0 = __shfl_sync(0xffffffffu, r.q0, src);
+        it.rows = __shfl_sync(0xffffffffu, r.nq, src) * p.group;
+        it.len = __shfl_sync(0xffffffffu, r.len, src);
+        it.first = __shfl_sync(0xffffffffu, r.first, src);
+        it.lo = __shfl_sync(0xffffffffu, r.lo, src);
+        // keys that any row of the item sees, in blocks; this split's share of the blocks
+        const int last_tok = (min(it.rows, it.row0 + kKpRows) - 1) / p.group, first_tok = it.row0 / p.group;
+        const int hi = max(0, p.causal ? min(it.len, it.first + last_tok + 1) : it.len);
+        const int lo = p.window > 0 ? max(0, it.first + first_tok - p.window + 1) : 0;
+        const int blk0 = lo / kKpBlock, blocks = max(0, (hi + kKpBlock - 1) / kKpBlock - blk0);
+        const int j0 = static_cast<int>(static_cast<int64_t>(blocks) * it.split / pp.splits);
+        it.n = static_cast<int>(static_cast<int64_t>(blocks) * (it.split + 1) / pp.splits) - j0;
+        it.t_first = (blk0 + j0) * kKpBlock;
+        return true;
+    }
+    return false;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kKpThreads, 1)
 kv4_prefill_kernel(const PrefillParams pp) {
     using L = KpLayout<D>;
     const AttnParams& p = pp.a;
     extern __shared__ uint8_t kp_raw[];
-    __shared__ __align__(8) uint64_t k_full[2], v_full[2], k_free[2], v_free[2], s_full[2], p_full[2], o_full[2];
-    __shared__ __align__(8) uint64_t q_full, done_bar;
+    __shared__ __align__(16) uint4 clc_answer;
+    __shared__ __align__(8) uint64_t k_full[2], v_full[2], k_free[2], v_free[2];
+    __shared__ __align__(8) uint64_t s_full[2][2], p_full[2][2], o_full[2][2];     // [tile][buffer]
+    __shared__ __align__(8) uint64_t q_full[2], item_full, item_free, clc_bar, done_bar[2];
+    __shared__ KpItem s_item;
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag, s_b, s_tile;
-    __shared__ int scan[kKpThreads / 32];
+    __shared__ int abort_flag;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(kp_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sbase = smem_u32(smem);
     pdl_launch_dependents();
     pdl_wait();
-
-    // ---- this CTA's row tile: the last ones first (they see the most keys)
-    const int per = (p.B + kKpThreads - 1) / kKpThreads;
-    const int rb0 = min(p.B, tid * per), rb1 = min(p.B, rb0 + per);
-    int mine = 0;
-    for (int b = rb0; b < rb1; ++b) mine += kp_tiles(p, kv4_request(p, b));
-    int incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += a;
-    }
-    if (lane == 31) scan[warp] = incl;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&k_full[i], 4);       // the decoding warps
             mbar_init(&v_full[i], 4);
-            mbar_init(&k_free[i], 1);
-            mbar_init(&v_free[i], 1);
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);       // a tile's softmax warps
-            mbar_init(&o_full[i], 1);
+            mbar_init(&k_free[i], 2);       // the issuing warps
+            mbar_init(&v_free[i], 2);
+            mbar_init(&q_full[i], 4);       // a tile's softmax warps
+            mbar_init(&done_bar[i], 1);
+            for (int u = 0; u < 2; ++u) {
+                mbar_init(&s_full[i][u], 1);
+                mbar_init(&p_full[i][u], 4);
+                mbar_init(&o_full[i][u], 1);
+            }
         }
-        mbar_init(&q_full, 8);
-        mbar_init(&done_bar, 1);
+        mbar_init(&item_full, 1);
+        mbar_init(&item_free, 14);          // softmax, decoding and issuing warps
+        mbar_init(&clc_bar, 1);
         abort_flag = 0;
-        s_b = -1;
         fence_mbar_init();
     }
-    __syncthreads();
-    int before = incl - mine, total = 0;
-    for (int w = 0; w < kKpThreads / 32; ++w) {
-        if (w < warp) before += scan[w];
-        total += scan[w];
-    }
-    const int kvh = static_cast<int>(blockIdx.x) % p.c.heads;
-    const int want = total - 1 - static_cast<int>(blockIdx.x) / p.c.heads;
-    if (want >= before && want < before + mine) {
-        int at = before;
-        for (int b = rb0; b < rb1; ++b) {
-            const int n = kp_tiles(p, kv4_request(p, b));
-            if (want < at + n) {
-                s_b = b;
-                s_tile = want - at;
-                break;
-            }
-            at += n;
-        }
-    }
-    __syncthreads();
-    if (s_b < 0) return;
-    const int b = s_b;
-    const Request r = kv4_request(p, b);
-    const int rows = r.nq * p.group, row0 = s_tile * kKpRows;
-    const bool two = row0 + 128 < rows;                    // the second tile has rows
-    // keys that any row of the CTA sees, in blocks; this split's share of the blocks
-    const int last_tok = (min(rows, row0 + kKpRows) - 1) / p.group, first_tok = row0 / p.group;
-    const int hi = max(0, p.causal ? min(r.len, r.first + last_tok + 1) : r.len);
-    const int lo = p.window > 0 ? max(0, r.first + first_tok - p.window + 1) : 0;
-    const int blk0 = lo / kKpBlock, blocks = max(0, (hi + kKpBlock - 1) / kKpBlock - blk0);
-    const int split = blockIdx.y;
-    const int j0 = static_cast<int>(static_cast<int64_t>(blocks) * split / pp.splits);
-    const int n = static_cast<int>(static_cast<int64_t>(blocks) * (split + 1) / pp.splits) - j0;
-    const int t_first = (blk0 + j0) * kKpBlock;
-    const int page = p.c.page, sh = __ffs(page) - 1;
-
     if (warp == 12) {
         tmem_alloc(&tmem_slot, 512);
         tmem_relinquish();
@@ -236,266 +265,390 @@ kv4_prefill_kernel(const PrefillParams pp) {
     const uint32_t tmem = tmem_slot;
     volatile int* abort = &abort_flag;
     const uint64_t limit = p.limit_ns;
+    const int page = p.c.page, sh = __ffs(page) - 1;
+    // waits of a converged warp: all lanes go on, or none
+    auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1u, abort, limit));
+    };
+    // The next item (k counts them); `release`: give the slot back at once.
+    auto next_item = [&](KpItem& it, uint32_t k, bool release) -> bool {
+        if (!wait(&item_full, k)) return false;
+        it = s_item;
+        __syncwarp();
+        if (release && lane == 0) mbar_arrive(&item_free);
+        return it.state > 0;
+    };
 
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kKpRegsSoftmax));
         // -------------------------------------------------------------- softmax
         const int x = warp >> 2;                           // tile
-        const int row = row0 + x * 128 + (tid & 127);
-        const bool in = row < rows;
-        const int tok = in ? row / p.group : 0;
-        const int head = kvh * p.group + (in ? row - tok * p.group : 0);
-        {
-            // this thread's row of Q, operand layout, channels in the decode's order
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + (r.q0 + tok) * p.q_stride + static_cast<int64_t>(head) * D);
-            const uint32_t at = sbase + L::kQ + x * L::kTile + static_cast<uint32_t>(tid & 127) * 128u;
-            const uint32_t sw = static_cast<uint32_t>(tid) & 7u;
-#pragma unroll
-            for (int w = 0; w < D / 8; ++w) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (in) v = __ldg(src + w);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                             :: "r"(at + static_cast<uint32_t>(w >> 3) * kKpHalf + ((static_cast<uint32_t>(w & 7) ^ sw) << 4)),
-                                "r"(__byte_perm(v.x, v.z, 0x5410)), "r"(__byte_perm(v.x, v.z, 0x7632)),
-                                "r"(__byte_perm(v.y, v.w, 0x5410)), "r"(__byte_perm(v.y, v.w, 0x7632))
-                             : "memory");
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_full);
-        }
-        const int pos = r.first + tok;
-        // rows past the last query see everything: their zero queries are harmless, and masks stay rare
-        const int lim = !in ? 0x7fffffff : p.causal ? pos : r.len - 1;
-        const int low = in && p.window > 0 ? pos - p.window + 1 : 0;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
         const uint32_t ts = lanes + static_cast<uint32_t>(x) * 128u, to = lanes + L::kO + static_cast<uint32_t>(x) * D;
-        const uint32_t tp = lanes + L::kP + static_cast<uint32_t>(x) * L::kPStride;
         const float c = p.scale_log2;
+        const int64_t all = static_cast<int64_t>(p.N) * p.Hq;
+        KpItem it;
+        uint32_t cnt = 0;                                  // 64-key steps of this tile so far
+        // the item before, whose rows are still in TMEM
+        bool held = false, held_in = false;
+        int held_n = 0, held_split = 0;
+        int64_t held_at = 0;
         float m = -INFINITY, l = 0.0f;
-        bool ok = true;
-        const int np = kKpBlock >> sh;                     // pages per block
-        for (int j = 0; j < n && (x == 0 || two); ++j) {
-            const int t0 = t_first + j * kKpBlock;
-            // pages the table does not name (checked by the first lanes while the scores are computed)
-            int id = 0;
-            if (lane < np && t0 + lane * page < r.len) {
-                id = __ldg(p.table + b * p.table_stride + ((t0 >> sh) + lane));
-                id = id < 0 || id >= p.c.pages ? -1 : 0;
-            }
-            const uint32_t gone = __ballot_sync(0xffffffffu, id < 0);
-            ok = mbar_wait(&s_full[x], static_cast<uint32_t>(j) & 1u, abort, limit);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-            uint32_t s[4][32];
+        for (uint32_t k = 0;; ++k) {
+            const bool more = next_item(it, k, true);
+            const bool mine = more && (x == 0 || it.row0 + 128 < it.rows);
+            const int row = it.row0 + x * 128 + (tid & 127);
+            const bool in = mine && row < it.rows;
+            const int tok = in ? row / p.group : 0;
+            const int head = it.kvh * p.group + (in ? row - tok * p.group : 0);
+            if (mine) {
+                // this thread's row of Q, operand layout, channels in the decode's order.  The scores of the item
+                // before have been waited for, so nothing reads the buffer any more.
+                const uint4* src = reinterpret_cast<const uint4*>(p.q + (it.q0 + tok) * p.q_stride + static_cast<int64_t>(head) * D);
+                const uint32_t at = sbase + L::kQ + x * L::kTile + static_cast<uint32_t>(tid & 127) * 128u;
+                const uint32_t sw = static_cast<uint32_t>(tid) & 7u;
+                uint4 v[D / 8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(ts + 32 * q, s[q]);
-            tmem_ld_wait();
-            const bool plain = gone == 0 && t0 + kKpBlock <= r.len && lim >= t0 + kKpBlock - 1 && low <= t0;
-            if (!__all_sync(0xffffffffu, plain)) {
-                const int top = min(lim, r.len - 1);
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int tk = t0 + 32 * q + i;
-                        if (tk > top || tk < low || ((gone >> ((32 * q + i) >> sh)) & 1u)) s[q][i] = 0xff800000u;   // -inf
-                    }
-            }
-            float mx[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                mx[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
-#pragma unroll
-                for (int i = 2; i < 32; i += 2)
-                    mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])));
-            }
-            const float xm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-            const bool grow = xm > m + kKaGrow;
-            if (__any_sync(0xffffffffu, grow)) {
-                const float a = grow ? ex2(m - xm) : 1.0f;
-                if (grow) m = xm;
-                l *= a;
-                if (j > 0) {
-                    // the product of the block before has completed: it was issued before this block's scores
-#pragma unroll 1
-                    for (int q = 0; q < D / 32; ++q) {
-                        uint32_t o[32];
-                        tmem_ld_32x32b_x32(to + 32 * q, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-                        tmem_st_32x32b_x32(to + 32 * q, o);
-                    }
+                for (int w = 0; w < D / 8; ++w) {
+                    v[w] = make_uint4(0u, 0u, 0u, 0u);
+                    if (in) v[w] = __ldg(src + w);
                 }
+#pragma unroll
+                for (int w = 0; w < D / 8; ++w)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                                 :: "r"(at + static_cast<uint32_t>(w >> 3) * kKpHalf + ((static_cast<uint32_t>(w & 7) ^ sw) << 4)),
+                                    "r"(__byte_perm(v[w].x, v[w].z, 0x5410)), "r"(__byte_perm(v[w].x, v[w].z, 0x7632)),
+                                    "r"(__byte_perm(v[w].y, v[w].w, 0x5410)), "r"(__byte_perm(v[w].y, v[w].w, 0x7632))
+                                 : "memory");
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[x]);
             }
-            const float nm = m == -INFINITY ? 0.0f : -m;
-            const float2 c2 = make_float2(c, c), n2 = make_float2(nm, nm);
-            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t o[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float2 e = fma2(make_float2(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), c2, n2);
-                    e.x = ex2(e.x);
-                    e.y = ex2(e.y);
-                    sum[i & 1] = add2(sum[i & 1], e);
-                    o[i] = pack_bf16(e.x, e.y);
+            if (held) {
+                // ---------------- the rows of the item before out, or their piece into the workspace
+                if (held_n > 0) {
+                    if (!wait(&o_full[x][(cnt - 1) & 1u], (cnt - 1) >> 1)) break;
+                    tc_fence_after();
                 }
-                tmem_st_32x32b_x16(tp + 16 * q, o);
-            }
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[x]);
-        }
-        // ---------------- the rows out, or their piece into the workspace
-        if (x == 0 || two) {
-            if (n > 0 && ok) {
-                ok = mbar_wait(&o_full[x], 0, abort, limit);
-                ok = __all_sync(0xffffffffu, ok);
-                tc_fence_after();
-            }
-            const int64_t at = static_cast<int64_t>(r.q0 + tok) * p.Hq + head;
-            const int64_t all = static_cast<int64_t>(p.N) * p.Hq;
-            const bool whole = pp.splits == 1;
-            const float f = !whole ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
-            if (ok) {
+                const bool whole = pp.splits == 1;
+                const float f = !whole ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll 1
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t o[32];
-                    if (n > 0) {
+                    if (held_n > 0) {
                         tmem_ld_32x32b_x32(to + 32 * q, o);
                         tmem_ld_wait();
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = 0u;
                     }
-                    if (!in) continue;
+                    if (!held_in) continue;
                     float v[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i)           // column 8w + (0..7) holds channel 8w + (0, 4, 1, 5, 2, 6, 3, 7)
                         v[(i & ~7) + ((i & 7) >> 1) + 4 * (i & 1)] = __uint_as_float(o[i]) * f;
                     if (whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(p.out + at * D + 32 * q);
+                        uint4* dst = reinterpret_cast<uint4*>(p.out + held_at * D + 32 * q);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             dst[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
                                                 pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
                     } else {
-                        float4* dst = reinterpret_cast<float4*>(pp.part + (split * all + at) * D + 32 * q);
+                        float4* dst = reinterpret_cast<float4*>(pp.part + (held_split * all + held_at) * D + 32 * q);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                     }
                 }
-                if (in) {
+                if (held_in) {
                     if (whole) {
-                        if (p.lse) p.lse[at] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                        if (p.lse) p.lse[held_at] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
                     } else {
                         float* st = pp.part + pp.splits * all * D;
-                        st[split * all + at] = m;
-                        st[(pp.splits + split) * all + at] = l;
+                        st[held_split * all + held_at] = m;
+                        st[(pp.splits + held_split) * all + held_at] = l;
                     }
                 }
+                held = false;
             }
+            if (!more) break;
+            if (!mine) continue;
+            const int pos = it.first + tok;
+            // rows past the last query see everything: their zero queries are harmless, and masks stay rare
+            const int lim = !in ? 0x7fffffff : p.causal ? pos : it.len - 1;
+            const int low = in && p.window > 0 ? pos - p.window + 1 : 0;
+            m = -INFINITY;
+            l = 0.0f;
+            const int steps = 2 * it.n;
+            const int top = min(lim, it.len - 1);
+            const int warp_top = __reduce_min_sync(0xffffffffu, top), warp_low = __reduce_max_sync(0xffffffffu, low);
+            const int* const trow = p.table + it.b * p.table_stride;
+            bool ok = true;
+            // a lane's page of a block: -1 where the table names none (then its tokens are left out)
+            auto entry = [&](int t0) -> int {
+                const int t = t0 + lane * page;
+                if (lane >= (kKpBlock >> sh) || t >= it.len) return 0;
+                const int id = __ldg(trow + (t >> sh));
+                return id < 0 || id >= p.c.pages ? -1 : 0;
+            };
+            int id = entry(it.t_first);
+            uint32_t gone = 0;
+            for (int i = 0; i < steps; ++i, ++cnt) {
+                const int t0 = it.t_first + 64 * i;
+                const uint32_t u = cnt & 1u, tsu = ts + 64u * u;
+                if ((i & 1) == 0) {
+                    gone = __ballot_sync(0xffffffffu, id < 0);
+                    id = entry(t0 + kKpBlock);
+                }
+                ok = wait(&s_full[x][u], cnt >> 1);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t s[64];
+                tmem_ld_32x32b_x32(tsu, reinterpret_cast<uint32_t (&)[32]>(s[0]));
+                tmem_ld_32x32b_x32(tsu + 32u, reinterpret_cast<uint32_t (&)[32]>(s[32]));
+                tmem_ld_wait();
+                if (gone != 0 || warp_top < t0 + 63 || warp_low > t0) {
+                    const int in_block = 64 * (i & 1);
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) {
+                        const int tk = t0 + e;
+                        if (tk > top || tk < low || ((gone >> ((in_block + e) >> sh)) & 1u)) s[e] = 0xff800000u;   // -infinity
+                    }
+                }
+                float mx[2] = {max3(s[0], s[1], s[2]), max3(s[3], s[4], s[5])};
+#pragma unroll
+                for (int e = 6; e < 62; e += 4) {
+                    mx[0] = max3(__float_as_uint(mx[0]), s[e], s[e + 1]);
+                    mx[1] = max3(__float_as_uint(mx[1]), s[e + 2], s[e + 3]);
+                }
+                const float xm = max3(__float_as_uint(fmaxf(mx[0], mx[1])), s[62], s[63]) * c;
+                const bool grow = xm > m + kKaGrow;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float a = grow ? ex2(m - xm) : 1.0f;
+                    if (grow) m = xm;
+                    l *= a;
+                    if (i > 0) {
+                        // O holds the steps before: their products must have completed
+                        ok = wait(&o_full[x][u ^ 1u], (cnt - 1) >> 1);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int q = 0; q < D / 16; ++q) {
+                            uint32_t y[16];
+                            tmem_ld_32x32b_x16(to + 16 * q, y);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * a);
+                            tmem_st_32x32b_x16(to + 16 * q, y);
+                        }
+                    }
+                }
+                const float nm = m == -INFINITY ? 0.0f : -m;
+                const float2 c2 = make_float2(c, c), n2 = make_float2(nm, nm);
+                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                // P over its S (every lane of the warp has read its own)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t o[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float2 w = fma2(make_float2(__uint_as_float(s[32 * q + 2 * e]), __uint_as_float(s[32 * q + 2 * e + 1])), c2, n2);
+                        w.x = ex2(w.x);
+                        w.y = ex2(w.y);
+                        sum[e & 1] = add2(sum[e & 1], w);
+                        o[e] = pack_bf16(w.x, w.y);
+                    }
+                    tmem_st_32x32b_x16(tsu + 16u * q, o);
+                }
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[x][u]);
+            }
+            if (!ok) break;
+            held = true;
+            held_in = in;
+            held_n = it.n;
+            held_split = it.split;
+            held_at = static_cast<int64_t>(it.q0 + tok) * p.Hq + head;
         }
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kKpRegsDecode));
         // ------------------------------------------------------------- decoding
         const int me = tid & 127;                          // token of the block
-        auto cell_of = [&](int j, bool& live) -> int64_t {
-            const int t = t_first + j * kKpBlock + me;
-            live = j < n && t < r.len && t >= r.lo;
-            int id = 0;
-            if (live) {
-                id = __ldg(p.table + b * p.table_stride + (t >> sh));
-                live = id >= 0 && id < p.c.pages;
-            }
-            return (static_cast<int64_t>(id) * p.c.heads + kvh) * page + (t & (page - 1));
-        };
-        KpRow<D> kr, vr;
-        bool live;
-        int64_t cell = cell_of(0, live);
-        kp_load<D>(kr, p.c.kc, p.c.ks, cell, live);
-        kp_load<D>(vr, p.c.vc, p.c.vs, cell, live);
-        for (int j = 0; j < n; ++j) {
-            const int u = j & 1;
-            const uint32_t par = (static_cast<uint32_t>(j >> 1) & 1u) ^ 1u;
-            cell = cell_of(j + 1, live);
-            bool ok = mbar_wait(&k_free[u], par, abort, limit);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            kp_decode<D>(kr, sbase + L::kK + u * L::kTile, me);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&k_full[u]);
+        KpItem it;
+        uint32_t cnt = 0;                                  // blocks so far
+        bool ok = true;
+        for (uint32_t k = 0; ok && next_item(it, k, false); ++k) {
+            auto cell_of = [&](int j, bool& live) -> int64_t {
+                const int t = it.t_first + j * kKpBlock + me;
+                live = j < it.n && t < it.len && t >= it.lo;
+                int id = 0;
+                if (live) {
+                    id = __ldg(p.table + it.b * p.table_stride + (t >> sh));
+                    live = id >= 0 && id < p.c.pages;
+                }
+                return (static_cast<int64_t>(id) * p.c.heads + it.kvh) * page + (t & (page - 1));
+            };
+            KpRow<D> kr, vr;
+            bool live;
+            int64_t cell = cell_of(0, live);
             kp_load<D>(kr, p.c.kc, p.c.ks, cell, live);
-            ok = mbar_wait(&v_free[u], par, abort, limit);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            kp_decode<D>(vr, sbase + L::kV + u * L::kTile, me);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&v_full[u]);
             kp_load<D>(vr, p.c.vc, p.c.vs, cell, live);
+            const int last = max(0, it.n - 2);             // from here on the next item is wanted
+            for (int j = 0; j < it.n; ++j, ++cnt) {
+                if (j == last && lane == 0) mbar_arrive(&item_free);
+                const uint32_t u = cnt & 1u, par = (cnt >> 1) ^ 1u;
+                cell = cell_of(j + 1, live);
+                ok = wait(&k_free[u], par);
+                if (!ok) break;
+                kp_decode<D>(kr, sbase + L::kK + u * L::kTile, me);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&k_full[u]);
+                kp_load<D>(kr, p.c.kc, p.c.ks, cell, live);
+                ok = wait(&v_free[u], par);
+                if (!ok) break;
+                kp_decode<D>(vr, sbase + L::kV + u * L::kTile, me);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&v_full[u]);
+                kp_load<D>(vr, p.c.vc, p.c.vs, cell, live);
+            }
+            if (it.n == 0 && lane == 0) mbar_arrive(&item_free);
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kKpRegsIssue));
-        if (warp == 12 && lane == 0) {
-            // ---------------------------------------------------------- products
-            // kind::f16, D float32, A and B bf16; S: N = 128, both K-major; O: N = D, B MN-major
-            constexpr uint32_t id_s = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+        if (warp < 14) {
+            // ---------------------------------------------------------- products of tile x
+            // The whole warp walks the loop and one elected lane issues, so addresses and descriptors stay
+            // warp-uniform.  kind::f16, D float32, A and B bf16; S: N = 64, both K-major; O: N = D, B MN-major.
+            constexpr uint32_t id_s = (1u << 4) | (1u << 7) | (1u << 10) | ((64u >> 3) << 17) | ((128u >> 4) << 24);
             constexpr uint32_t id_o = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((static_cast<uint32_t>(D) >> 3) << 17) |
                                       ((128u >> 4) << 24);
-            auto scores = [&](int x, int j) {
-                const uint32_t qa = sbase + L::kQ + x * L::kTile, kb = sbase + L::kK + (j & 1) * L::kTile;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = static_cast<uint32_t>(kk & 3) * 32u + static_cast<uint32_t>(kk >> 2) * kKpHalf;
-                    tc_mma_f16(tmem + x * 128u, smem_desc_k_sw128(qa + off), smem_desc_k_sw128(kb + off), id_s, kk > 0);
+            const int x = warp - 12;
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint64_t dq = smem_desc_k_sw128(__shfl_sync(0xffffffffu, sbase, 0)) + ((L::kQ + x * L::kTile) >> 4);
+            const uint64_t dk = smem_desc_k_sw128(__shfl_sync(0xffffffffu, sbase, 0)) + (L::kK >> 4);
+            const uint64_t dv = smem_desc_mn_sw128(__shfl_sync(0xffffffffu, sbase, 0)) + (L::kV >> 4);
+            const uint32_t ts = tm + x * 128u, to = tm + L::kO + x * D;
+            const bool leader = elect_one();
+            KpItem it;
+            uint32_t cnt = 0, blk = 0, items = 0;          // this tile's 64-key steps, all blocks, this tile's items
+            bool ok = true;
+            for (uint32_t k = 0; ok && next_item(it, k, true); ++k) {
+                if (x == 1 && it.row0 + 128 >= it.rows) {
+                    // no rows in this tile: the blocks are the other tile's alone
+                    for (int j = 0; ok && j < it.n; ++j, ++blk) {
+                        ok = wait(&k_full[blk & 1u], blk >> 1) && wait(&v_full[blk & 1u], blk >> 1);
+                        if (ok && leader) {
+                            mbar_arrive(&k_free[blk & 1u]);
+                            mbar_arrive(&v_free[blk & 1u]);
+                        }
+                        __syncwarp();
+                    }
+                    continue;
                 }
-                tc_commit(&s_full[x]);
-            };
-            auto output = [&](int x, int j) {
-                const uint32_t vb = sbase + L::kV + (j & 1) * L::kTile;
+                // scores of step i into buffer (cnt + i) & 1: keys 64 (i & 1) .. of block i / 2
+                auto scores = [&](int i) -> bool {
+                    const uint32_t bb = blk + static_cast<uint32_t>(i >> 1), u = (cnt + i) & 1u;
+                    if ((i & 1) == 0 && !wait(&k_full[bb & 1u], bb >> 1)) return false;
+                    tc_fence_after();
+                    const uint64_t kb = dk + (((bb & 1u) * L::kTile + (i & 1) * 8192u) >> 4);
+                    if (leader) {
 #pragma unroll
-                for (int kk = 0; kk < kKpBlock / 16; ++kk)
-                    tc_mma_f16_ts(tmem + L::kO + x * D, tmem + L::kP + x * L::kPStride + kk * 8,
-                                  smem_desc_mn_sw128(vb + kk * 2048u), id_o, j > 0 || kk > 0);
-            };
-            const int tiles = two ? 2 : 1;
-            bool ok = n > 0 && mbar_wait(&q_full, 0, abort, limit) && mbar_wait(&k_full[0], 0, abort, limit);
-            if (ok) {
-                tc_fence_after();
-                for (int x = 0; x < tiles; ++x) scores(x, 0);
-                tc_commit(&k_free[0]);
-            }
-            for (int j = 0; ok && j < n; ++j) {
-                const uint32_t par = static_cast<uint32_t>(j >> 1) & 1u;
-                ok = mbar_wait(&v_full[j & 1], par, abort, limit);
-                for (int x = 0; ok && x < tiles; ++x) {
-                    ok = mbar_wait(&p_full[x], static_cast<uint32_t>(j) & 1u, abort, limit);
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = (static_cast<uint32_t>(kk & 3) * 32u + static_cast<uint32_t>(kk >> 2) * kKpHalf) >> 4;
+                            tc_mma_f16(ts + 64u * u, dq + off, kb + off, id_s, kk > 0);
+                        }
+                        tc_commit(&s_full[x][u]);
+                        if (i & 1) tc_commit(&k_free[bb & 1u]);
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                const int steps = 2 * it.n;
+                ok = wait(&q_full[x], items);
+                ++items;
+                for (int i = 0; ok && i < 2 && i < steps; ++i) {
+                    // the item before: the product that reads this buffer's P
+                    const uint32_t g = cnt + static_cast<uint32_t>(i);
+                    ok = (g < 2 || wait(&o_full[x][g & 1u], (g - 2) >> 1)) && scores(i);
+                }
+                for (int i = 0; ok && i < steps; ++i) {
+                    const uint32_t bb = blk + static_cast<uint32_t>(i >> 1), u = (cnt + i) & 1u;
+                    if ((i & 1) == 0) ok = wait(&v_full[bb & 1u], bb >> 1);
+                    ok = ok && wait(&p_full[x][u], (cnt + i) >> 1);
                     if (!ok) break;
                     tc_fence_after();
-                    output(x, j);
-                    if (x == tiles - 1) tc_commit(&v_free[j & 1]);
-                    if (j + 1 == n) {
-                        tc_commit(&o_full[x]);
-                        continue;
+                    const uint64_t vb = dv + (((bb & 1u) * L::kTile + (i & 1) * 8192u) >> 4);
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma_f16_ts(to, ts + 64u * u + kk * 8, vb + (kk * 2048u >> 4), id_o, i > 0 || kk > 0);
+                        tc_commit(&o_full[x][u]);
+                        if (i & 1) tc_commit(&v_free[bb & 1u]);
                     }
-                    if (x == 0) {
-                        ok = mbar_wait(&k_full[(j + 1) & 1], static_cast<uint32_t>((j + 1) >> 1) & 1u, abort, limit);
-                        if (!ok) break;
-                        tc_fence_after();
+                    __syncwarp();
+                    if (i + 2 < steps) {
+                        // the next scores of this buffer overwrite the P that the product above reads
+                        ok = wait(&o_full[x][u], (cnt + i) >> 1) && scores(i + 2);
                     }
-                    scores(x, j + 1);
-                    if (x == tiles - 1) tc_commit(&k_free[(j + 1) & 1]);
                 }
+                cnt += steps;
+                blk += it.n;
             }
             // every MMA must have retired before TMEM is released
-            tc_commit(&done_bar);
-            mbar_wait(&done_bar, 0, nullptr, kDrainLimitNs);
+            if (leader) tc_commit(&done_bar[x]);
+            __syncwarp();
+            mbar_wait(&done_bar[x], 0, nullptr, kDrainLimitNs);
+        } else if (warp == 14) {
+            // ---------------------------------------------------------- the items
+            int idx = static_cast<int>(blockIdx.x);
+            uint32_t k = 0, asked = 0;
+            bool ok = true, more = true;
+            while (ok) {
+                KpItem it;
+                const bool work = more && kp_locate(pp, idx, lane, it);
+                if (work || !more) {
+                    if (k > 0) ok = wait(&item_free, k - 1);           // everyone has read the item before
+                    if (!ok) break;
+                    if (lane == 0) {
+                        if (!more) it.state = -1;
+                        s_item = it;
+                        mbar_arrive(&item_full);
+                    }
+                    __syncwarp();
+                    ++k;
+                    if (!more) break;
+                    ok = wait(&item_free, k - 1);                      // and wants the next one
+                    if (!ok) break;
+                }
+                // take over the next CTA that has not started
+                if (lane == 0) {
+                    fence_proxy_async_smem();
+                    mbar_arrive_expect_tx(&clc_bar, 16);
+                    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                                 :: "r"(smem_u32(&clc_answer)), "r"(smem_u32(&clc_bar)) : "memory");
+                }
+                __syncwarp();
+                ok = wait(&clc_bar, asked);
+                if (!ok) break;
+                ++asked;
+                uint32_t got, cx;
+                asm volatile(
+                    "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t.reg .b32 y, z, w;\n\t"
+                    "ld.shared.b128 a, [%2];\n\t"
+                    "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+                    "selp.u32 %0, 1, 0, p;\n\t"
+                    "mov.u32 %1, 0;\n\t"
+                    "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, a;\n\t}"
+                    : "=r"(got), "=r"(cx) : "r"(smem_u32(&clc_answer)) : "memory");
+                __syncwarp();
+                more = __shfl_sync(0xffffffffu, got, 0) != 0;
+                idx = static_cast<int>(__shfl_sync(0xffffffffu, cx, 0));
+            }
+            // an answer may not land after the CTA is gone: every request has been waited for, or the limit has run out
         }
         __syncwarp();
     }

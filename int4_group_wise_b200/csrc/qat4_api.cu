@@ -1103,7 +1103,8 @@ static bool kv4_decode_rows(const qat4::AttnParams& p, int64_t clusters, cudaStr
 
 template <int D>
 static bool kv4_prefill_launch(const qat4::PrefillParams& p, int64_t tiles, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(tiles * p.a.c.heads), static_cast<unsigned>(p.splits));
+    // one CTA per work item; those that have not started are taken over by the running ones
+    const dim3 grid(static_cast<unsigned>(tiles * p.a.c.heads * p.splits));
     if (!launch_pdl(qat4::kv4_prefill_kernel<D>, grid, qat4::kKpThreads, qat4::KpLayout<D>::kSmem, stream, 1, p)) return false;
     if (p.splits == 1) return true;
     const int64_t rows = static_cast<int64_t>(p.a.N) * p.a.Hq;
@@ -1157,8 +1158,9 @@ qat4_status qat4_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t N, i
     p.causal = causal;
     p.window = window;
     p.scale_log2 = scale * 1.4426950408889634f;
-    // generous bound of a wait: 10 s (a CTA waits for one unit's copies or one block's products, microseconds)
-    p.limit_ns = 10000000000ull;
+    // generous bound of a wait: 10 s, and 20 us for every 128 tokens that the table can name (the longest wait of
+    // a warp is for another tile's item, one or two microseconds per 128 tokens)
+    p.limit_ns = 10000000000ull + 20000ull * static_cast<uint64_t>(max_blocks * cache->page_size / 128);
     const Kv4Plan pl = kv4_plan(N, B, p.group, H);
     const int64_t clusters = pl.decode ? kv4_clusters(N, B, p.group, H, cache->page_size, max_blocks) : 0;
     bool ok = true;
