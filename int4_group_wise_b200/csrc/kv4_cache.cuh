@@ -199,8 +199,8 @@ __device__ __forceinline__ float kv4_step(float m) {
     return d < 0x1p-100f ? 0.0f : fminf(up, 0x1p100f);
 }
 
-// Eight values as packed codes, two's-complement nibbles, value i at bits 4i.
-__device__ __forceinline__ uint32_t kv4_pack8(const float (&v)[8], float step) {
+// Eight values as packed codes, two's-complement nibbles, value i at bits 4i.  Any step and any values.
+__device__ __noinline__ uint32_t kv4_pack8_any(const float (&v)[8], float step) {
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -209,62 +209,128 @@ __device__ __forceinline__ uint32_t kv4_pack8(const float (&v)[8], float step) {
     }
     return w;
 }
+// The same for groups whose largest magnitude m is at most 2^102, with the step.  Both quotients, fl(m / 7)
+// and fl(v / step), come from an approximate reciprocal r (within 1 ulp) by Markstein's correction
+// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990):
+// q0 = fl(v r), e = v - q0 d exactly by one FMA, q = fl(q0 + e r).  A quotient of a 24-bit significand by one
+// of at most 5 bits is at least 2^-31 of itself from the nearest rounding boundary, and q0 + e r within 2^-44,
+// so q is the IEEE quotient (below 2^-100, where e may lose bits, the step is 0 and every code too).  Cutting
+// q to [-8, 7] before it is rounded changes no code; adding 1.5 * 2^23 rounds it half to even and leaves the
+// code in the low bits.
+__device__ __forceinline__ float kv4_quotient(float a, float d, float r) {
+    const float q0 = __fmul_rn(a, r);
+    return __fmaf_rn(__fmaf_rn(-q0, d, a), r, q0);
+}
+__device__ __forceinline__ uint32_t kv4_pack8(const float (&v)[8], float m, float& step) {
+    const float d = kv4_quotient(m, 7.0f, 1.0f / 7.0f);
+    const float up = __uint_as_float((__float_as_uint(d) + 0x7FFFFu) & ~0x7FFFFu);
+    step = d < 0x1p-100f ? 0.0f : fminf(up, 0x1p100f);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(step));
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 7; i >= 0; --i) {
+        const float q = kv4_quotient(v[i], step, r);
+        const uint32_t c = __float_as_uint(__fadd_rn(fminf(fmaxf(q, kQmin), kQmax), 12582912.0f));
+        w = (w << 4) | (c & 15u);
+    }
+    return step == 0.0f ? 0u : w;
+}
 
 constexpr int kKvBlock = 256;
+constexpr int kKvItems = 4;                        // 8-channel words per thread of large batches, loaded together
 
-// Thread = 8 channels of one token and head of k or v; four neighbouring lanes
-// hold a group and find its largest magnitude by two shuffles.  One pass: each
-// value is read once, codes leave as one 4-byte word per lane.
-template <bool BF16>
+// How blocks cover the words of n tokens of k (blockIdx.y = 0) or v (1): `tokens` whole tokens per block, or
+// one token in `parts` blocks when it has more words than a block takes.
+struct Kv4Span {
+    int64_t n;
+    int row;                 // words of a token
+    uint32_t inv;            // floor(2^32 / row) + 1: quotients of indexes below 2^16 by a multiply
+    int tokens, parts, span; // span: words of a block
+};
+// Word `i` of this thread: its token, and the word inside the token; false past the end.
+__device__ __forceinline__ bool kv4_word(const Kv4Span& s, int i, int64_t& tok, int& rest) {
+    const uint32_t li = threadIdx.x + kKvBlock * i;
+    if (s.parts > 1) {
+        tok = blockIdx.x / s.parts;
+        rest = static_cast<int>(blockIdx.x - tok * s.parts) * s.span + static_cast<int>(li);
+        return rest < s.row;
+    }
+    const uint32_t t = s.row == 1 ? li : __umulhi(li, s.inv);
+    rest = static_cast<int>(li - t * s.row);
+    tok = static_cast<int64_t>(blockIdx.x) * s.tokens + t;
+    return static_cast<int>(t) < s.tokens && tok < s.n;
+}
+
+// Thread = 8 channels of a token and head, ITEMS of them at a time; four neighbouring lanes hold a group and
+// find its largest magnitude by two shuffles.  One pass: each value is read once, codes leave as one 4-byte
+// word per lane.  Bound: HBM (16411 tokens of 8 heads of 128, 67 MB in and 19 MB out, 13.4 us at the copy
+// rate: REPL_A).
+template <bool BF16, int ITEMS>
 __global__ void __launch_bounds__(kKvBlock)
-kv4_append_kernel(const Kv4View c, const void* __restrict__ k, const void* __restrict__ v, int64_t k_stride,
-                  int64_t v_stride, const int* __restrict__ slots, int64_t items) {
+kv4_append_kernel(const Kv4View c, const Kv4Span s, const void* __restrict__ k, const void* __restrict__ v,
+                  int64_t k_stride, int64_t v_stride, const int* __restrict__ slots) {
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kKvBlock + threadIdx.x;   // items is a multiple of 4
-    const bool in = i < 2 * items;
-    const bool isv = in && i >= items;
-    const int64_t u = in ? (isv ? i - items : i) : 0;
-    const int words = c.dim >> 3;                           // 8-channel words of a head
-    const int row = c.heads * words;
-    const int64_t tok = u / row;
-    const int rest = static_cast<int>(u - tok * row);
-    const int head = rest / words, w = rest - head * words;
-    const int slot = in ? __ldg(slots + tok) : -1;
-    const int sh = __ffs(c.page) - 1;
-    const bool live = slot >= 0 && (slot >> sh) < c.pages;
-    float x[8];
-    const int64_t at = tok * (isv ? v_stride : k_stride) + rest * 8;
-    if (BF16) {
-        uint4 r = make_uint4(0u, 0u, 0u, 0u);
-        if (live) r = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(isv ? v : k) + at));
-        const uint32_t q[4] = {r.x, r.y, r.z, r.w};
+    const bool isv = blockIdx.y != 0;
+    const void* const src = isv ? v : k;
+    const int64_t stride = isv ? v_stride : k_stride;
+    const int lw = c.dim == 128 ? 4 : 3, sh = __ffs(c.page) - 1;      // log2 of words per head
+    uint4 raw[ITEMS][BF16 ? 1 : 2];
+    int slot[ITEMS], at[ITEMS];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[2 * j] = __uint_as_float(q[j] << 16);
-            x[2 * j + 1] = __uint_as_float(q[j] & 0xFFFF0000u);
+    for (int i = 0; i < ITEMS; ++i) {
+        int64_t tok;
+        slot[i] = -1;
+#pragma unroll
+        for (int h = 0; h < (BF16 ? 1 : 2); ++h) raw[i][h] = make_uint4(0u, 0u, 0u, 0u);
+        if (kv4_word(s, i, tok, at[i])) {
+            slot[i] = __ldg(slots + tok);
+            if (slot[i] >= 0 && (slot[i] >> sh) < c.pages) {
+                const uint4* a = BF16 ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + tok * stride + at[i] * 8)
+                                      : reinterpret_cast<const uint4*>(static_cast<const float*>(src) + tok * stride + at[i] * 8);
+#pragma unroll
+                for (int h = 0; h < (BF16 ? 1 : 2); ++h) raw[i][h] = __ldcs(a + h);
+            } else {
+                slot[i] = -1;
+            }
         }
-    } else {
-        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
-        if (live) {
-            const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(isv ? v : k) + at);
-            a = __ldcs(s);
-            b = __ldcs(s + 1);
-        }
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
     }
-    float m = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    if (!live) return;
-    const float step = kv4_step(m);
-    const int64_t cell = (static_cast<int64_t>(slot >> sh) * c.heads + head) * c.page + (slot & (c.page - 1));
-    reinterpret_cast<uint32_t*>(isv ? c.vc : c.kc)[cell * words + w] = kv4_pack8(x, step);
-    if ((w & 3) == 0)
-        (isv ? c.vs : c.ks)[cell * (words >> 2) + (w >> 2)] = static_cast<uint16_t>(__float_as_uint(step) >> 16);
+    for (int i = 0; i < ITEMS; ++i) {
+        float x[8];
+        if (BF16) {
+            const uint32_t q[4] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[2 * j] = __uint_as_float(q[j] << 16);
+                x[2 * j + 1] = __uint_as_float(q[j] & 0xFFFF0000u);
+            }
+        } else {
+            const uint4 a = raw[i][0], b = raw[i][BF16 ? 0 : 1];
+            x[0] = __uint_as_float(a.x); x[1] = __uint_as_float(a.y); x[2] = __uint_as_float(a.z); x[3] = __uint_as_float(a.w);
+            x[4] = __uint_as_float(b.x); x[5] = __uint_as_float(b.y); x[6] = __uint_as_float(b.z); x[7] = __uint_as_float(b.w);
+        }
+        float m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));       // a group's four words are in one token: row is a
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));       // multiple of 8
+        if (slot[i] < 0) continue;
+        float step;
+        uint32_t word;
+        if (m <= 0x1p102f) {
+            word = kv4_pack8(x, m, step);
+        } else {
+            step = kv4_step(m);
+            word = kv4_pack8_any(x, step);
+        }
+        const int head = at[i] >> lw, w = at[i] & ((1 << lw) - 1);
+        const int64_t cell = (static_cast<int64_t>(slot[i] >> sh) * c.heads + head) * c.page + (slot[i] & (c.page - 1));
+        reinterpret_cast<uint32_t*>(isv ? c.vc : c.kc)[(cell << lw) + w] = word;
+        if ((w & 3) == 0)
+            (isv ? c.vs : c.ks)[(cell << (lw - 2)) + (w >> 2)] = static_cast<uint16_t>(__float_as_uint(step) >> 16);
+    }
 }
 
 // ------------------------------------------------------------------ gather
@@ -284,36 +350,44 @@ __device__ __forceinline__ uint32_t kv4_off(uint32_t step2) {
     return r;
 }
 
-// Thread = 8 channels of one token and head: 4 bytes of codes in, 16 bytes out; rows without a slot
-// are zero.
+// Thread = 8 channels of a token and head, ITEMS of them at a time: 4 bytes of codes in, 16 bytes out; rows
+// without a slot are zero.  Bound: HBM (19 MB in and 67 MB out for 16411 tokens of 8 heads of 128: REPL_G).
+template <int ITEMS>
 __global__ void __launch_bounds__(kKvBlock)
-kv4_gather_kernel(const Kv4View c, const int* __restrict__ slots, int64_t items, uint16_t* __restrict__ k,
+kv4_gather_kernel(const Kv4View c, const Kv4Span s, const int* __restrict__ slots, uint16_t* __restrict__ k,
                   uint16_t* __restrict__ v) {
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kKvBlock + threadIdx.x;
-    if (i >= 2 * items) return;
-    const bool isv = i >= items;
-    const int64_t u = isv ? i - items : i;
-    const int words = c.dim >> 3;
-    const int row = c.heads * words;
-    const int64_t tok = u / row;
-    const int rest = static_cast<int>(u - tok * row);
-    const int head = rest / words, w = rest - head * words;
-    const int slot = __ldg(slots + tok);
-    const int sh = __ffs(c.page) - 1;
-    uint4 o = make_uint4(0u, 0u, 0u, 0u);
-    if (slot >= 0 && (slot >> sh) < c.pages) {
+    const bool isv = blockIdx.y != 0;
+    const int lw = c.dim == 128 ? 4 : 3, sh = __ffs(c.page) - 1;
+    const uint32_t* const codes = reinterpret_cast<const uint32_t*>(isv ? c.vc : c.kc);
+    const uint16_t* const steps = isv ? c.vs : c.ks;
+    uint32_t q[ITEMS], st[ITEMS];
+    int64_t to[ITEMS];
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        int64_t tok;
+        int rest;
+        to[i] = -1;
+        q[i] = st[i] = 0;
+        if (!kv4_word(s, i, tok, rest)) continue;
+        to[i] = tok * s.row + rest;
+        const int slot = __ldg(slots + tok);
+        if (slot < 0 || (slot >> sh) >= c.pages) continue;
+        const int head = rest >> lw, w = rest & ((1 << lw) - 1);
         const int64_t cell = (static_cast<int64_t>(slot >> sh) * c.heads + head) * c.page + (slot & (c.page - 1));
-        const uint32_t q = reinterpret_cast<const uint32_t*>(isv ? c.vc : c.kc)[cell * words + w];
-        const uint32_t s = (isv ? c.vs : c.ks)[cell * (words >> 2) + (w >> 2)];
-        const uint32_t s2 = s | (s << 16), o2 = kv4_off(s2);
-        const uint32_t a = kv4_pair(q << 3, s2, o2), b = kv4_pair(q >> 1, s2, o2);      // channels (0, 4), (1, 5)
-        const uint32_t e = kv4_pair(q >> 5, s2, o2), f = kv4_pair(q >> 9, s2, o2);      // (2, 6), (3, 7)
-        o = make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(e, f, 0x5410), __byte_perm(a, b, 0x7632),
-                       __byte_perm(e, f, 0x7632));
+        q[i] = codes[(cell << lw) + w];
+        st[i] = steps[(cell << (lw - 2)) + (w >> 2)];
     }
-    reinterpret_cast<uint4*>(isv ? v : k)[u] = o;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        if (to[i] < 0) continue;
+        const uint32_t s2 = st[i] | (st[i] << 16), o2 = kv4_off(s2);
+        const uint32_t a = kv4_pair(q[i] << 3, s2, o2), b = kv4_pair(q[i] >> 1, s2, o2);      // channels (0, 4), (1, 5)
+        const uint32_t e = kv4_pair(q[i] >> 5, s2, o2), f = kv4_pair(q[i] >> 9, s2, o2);      // (2, 6), (3, 7)
+        __stcs(reinterpret_cast<uint4*>(isv ? v : k) + to[i],
+               make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(e, f, 0x5410), __byte_perm(a, b, 0x7632), __byte_perm(e, f, 0x7632)));
+    }
 }
 
 }  // namespace qat4
