@@ -1054,30 +1054,34 @@ static constexpr int kKaSms = 148;
 static constexpr int kKaGrid = 3 * kKaSms;       // most CTAs of the decode kernel
 
 // Which kernels serve a call, from what the host knows of it: N query tokens of B requests.
-//   average rows per request and kv head <= 32: the decode kernel takes every request (decode steps, drafts);
+//   average rows per request and kv head <= kRowsDecode: the decode kernel takes every request (decode steps,
+//   short drafts);
 //   more, and one request: the prefill kernel takes it;
 //   more, and several: requests of up to kRowsDecode rows go to the decode kernel, the others to the prefill
 //   kernel.
+// 16 requests of 700..6007 tokens, 32/8 heads of 128: 20 rows each take 64 us in the decode kernel and 68 in the
+// other, 36 rows 97 and 69.
+static constexpr int64_t kRowsDecode = 32;
 struct Kv4Plan {
     bool decode, prefill;
     int lo_decode, hi_decode, lo_prefill;
     int64_t tiles;        // upper bound of the prefill kernel's row tiles
-    int splits;           // most parts that the keys of a row tile are cut into
+    int splits;           // most parts that the keys of a row tile are cut into: two items per SM at most (16
+                          // requests of 36 rows: 92 us without, 69 with two items per SM, 75 with four)
 };
-static constexpr int kRowsDecode = 64;
 
 static Kv4Plan kv4_plan(int64_t N, int64_t B, int64_t group, int64_t kv_heads) {
     Kv4Plan pl = {true, false, 1, 0x7fffffff, 1, 0, 1};
     const int64_t rows = N * group;
-    if (rows <= 32 * B) return pl;
+    if (rows <= kRowsDecode * B) return pl;
     pl.prefill = true;
     pl.decode = B > 1;
     if (pl.decode) {
-        pl.hi_decode = kRowsDecode;
-        pl.lo_prefill = kRowsDecode + 1;
+        pl.hi_decode = static_cast<int>(kRowsDecode);
+        pl.lo_prefill = static_cast<int>(kRowsDecode) + 1;
     }
     pl.tiles = rows / qat4::kKpRows + std::min(B, rows / pl.lo_prefill);
-    pl.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, kKaSms / (pl.tiles * kv_heads))));
+    pl.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, 2 * kKaSms / (pl.tiles * kv_heads))));
     return pl;
 }
 
