@@ -264,8 +264,10 @@ __device__ __forceinline__ bool kv4_word(const Kv4Span& s, int i, int64_t& tok, 
 
 // Thread = 8 channels of a token and head, ITEMS of them at a time; four neighbouring lanes hold a group and
 // find its largest magnitude by two shuffles.  One pass: each value is read once, codes leave as one 4-byte
-// word per lane.  Bound: HBM (16411 tokens of 8 heads of 128, 67 MB in and 19 MB out, 13.4 us at the copy
-// rate: REPL_A).
+// word per lane.  16411 tokens of 8 heads of 128 (67 MB in, 19 MB out, 13.4 us at the copy rate) take 28.8 us:
+// the instructions of the quotients, codes and indexes (issue slots 75% busy) bound it, not the traffic; with
+// the codes replaced by a sum it takes 20.
+
 template <bool BF16, int ITEMS>
 __global__ void __launch_bounds__(kKvBlock)
 kv4_append_kernel(const Kv4View c, const Kv4Span s, const void* __restrict__ k, const void* __restrict__ v,
@@ -351,7 +353,8 @@ __device__ __forceinline__ uint32_t kv4_off(uint32_t step2) {
 }
 
 // Thread = 8 channels of a token and head, ITEMS of them at a time: 4 bytes of codes in, 16 bytes out; rows
-// without a slot are zero.  Bound: HBM (19 MB in and 67 MB out for 16411 tokens of 8 heads of 128: REPL_G).
+// without a slot are zero.  Bound: HBM (19 MB in and 67 MB out for 16411 tokens of 8 heads of 128: 13.4 us at the
+// copy rate, 16.3 measured).
 template <int ITEMS>
 __global__ void __launch_bounds__(kKvBlock)
 kv4_gather_kernel(const Kv4View c, const Kv4Span s, const int* __restrict__ slots, uint16_t* __restrict__ k,

@@ -13,9 +13,9 @@
 // next one that has not started (clusterlaunchcontrol), so the end of one item
 // overlaps the beginning of the next:
 //   warps 0-3, 4-7  softmax of tile 0 / 1, one thread per row, 64 keys at a time:
-//                   S from TMEM, exp2, P back to TMEM as bf16 over its S (the A
-//                   operand of the second product); O is rescaled in TMEM only
-//                   when the reference moves
+//                   S from TMEM, the maximum, exp2, P back to TMEM as bf16 over its
+//                   S (the A operand of the second product); O is rescaled in TMEM
+//                   only when the maximum grows by more than 2^8
 //   warps 8-11      decode the block's codes (one thread per token) into bf16
 //                   operands in shared memory, double buffered
 //   warps 12, 13    issue tile 0's / 1's MMAs: S = Q K^T (both K-major, N = 64) into
@@ -31,6 +31,18 @@
 //
 // With few row tiles the keys of each are cut into `splits` equal parts, which
 // leave (maximum, sum, unnormalised O) in the workspace for kv4_join_kernel.
+//
+// Measured on a B200 (calls replayed from a graph): a prompt of 4096 tokens with
+// 32/8 heads of 128, 147 us = 935 TFLOP/s; three chunks of 1501 tokens on 4674 to
+// 9001 cached ones with heads of 64, 377 us = 612 TFLOP/s.  What bounds it is the
+// round trip of a step (scores, softmax, P, product, and the buffer's next
+// scores), about 2000 clocks of which a thread's exponentials are 512: with them
+// left out the two calls still take 133 and 334 us, with the MMAs cut to an
+// eighth 104 and 267.  Tried and slower: one CTA per item without takeover (176
+// and 457 us), scores of 128 keys in one buffer (174 and 525), two threads a row
+// (161 and 512), weights taken against the maximum of the step before and redone
+// when they overflow (158 and 473), separate warps for S and O (154 and 385),
+// a quarter of the exponentials as polynomials (152 and 396).
 #pragma once
 
 #include "hessian.cuh"
@@ -38,9 +50,7 @@
 
 namespace qat4 {
 
-constexpr int kKpThreads = 512;                    // 2 softmax warpgroups, 1 decoding, 1 issuing
-constexpr int kKpRegsSoftmax = 176, kKpRegsDecode = 96, kKpRegsIssue = 64;   // per thread; their sum over the four
-                                                   // warpgroups is the 128 per thread of the launch
+constexpr int kKpThreads = 480;                    // 8 softmax, 4 decoding, 2 issuing warps, 1 for the items
 constexpr int kKpRows = 256;
 constexpr int kKpBlock = 128;                      // keys per block
 constexpr uint32_t kKpHalf = 128 * 128;            // 128 rows x 64 channels bf16: 16 KB
@@ -280,7 +290,6 @@ kv4_prefill_kernel(const PrefillParams pp) {
     };
 
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kKpRegsSoftmax));
         // -------------------------------------------------------------- softmax
         const int x = warp >> 2;                           // tile
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
@@ -473,7 +482,6 @@ kv4_prefill_kernel(const PrefillParams pp) {
             held_at = static_cast<int64_t>(it.q0 + tok) * p.Hq + head;
         }
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kKpRegsDecode));
         // ------------------------------------------------------------- decoding
         const int me = tid & 127;                          // token of the block
         KpItem it;
@@ -518,7 +526,6 @@ kv4_prefill_kernel(const PrefillParams pp) {
             if (it.n == 0 && lane == 0) mbar_arrive(&item_free);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kKpRegsIssue));
         if (warp < 14) {
             // ---------------------------------------------------------- products of tile x
             // The whole warp walks the loop and one elected lane issues, so addresses and descriptors stay

@@ -929,16 +929,6 @@ static bool kv4_decode_attr() {
            smem_attr(qat4::kv4_decode_kernel<D, ROWS, true>, qat4::KaLayout<D, ROWS>::kSmem);
 }
 
-// The prefill kernel's warpgroups trade registers: their shares must fit what the block is launched with, or
-// the growing ones would wait for good.
-template <int D>
-static bool kv4_prefill_attr() {
-    cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, qat4::kv4_prefill_kernel<D>) == cudaSuccess &&
-           at.numRegs * qat4::kKpThreads >= 128 * (2 * qat4::kKpRegsSoftmax + qat4::kKpRegsDecode + qat4::kKpRegsIssue) &&
-           smem_attr(qat4::kv4_prefill_kernel<D>, qat4::KpLayout<D>::kSmem);
-}
-
 // Shared-memory limits of the cache's kernels, once per context.
 static bool kv4_attrs(DeviceInfo* info) {
     std::lock_guard<std::mutex> lock(g_mutex);
@@ -947,7 +937,9 @@ static bool kv4_attrs(DeviceInfo* info) {
     if (!kv4_decode_attr<64, 4>() || !kv4_decode_attr<64, 8>() || !kv4_decode_attr<64, 16>() ||
         !kv4_decode_attr<128, 4>() || !kv4_decode_attr<128, 8>() || !kv4_decode_attr<128, 16>())
         return false;
-    if (!kv4_prefill_attr<64>() || !kv4_prefill_attr<128>()) return false;
+    if (!smem_attr(qat4::kv4_prefill_kernel<64>, qat4::KpLayout<64>::kSmem) ||
+        !smem_attr(qat4::kv4_prefill_kernel<128>, qat4::KpLayout<128>::kSmem))
+        return false;
     info->kv4_attr = true;
     return true;
 }
