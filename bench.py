@@ -983,6 +983,88 @@ def run_w4a16_decode(args):
         "stages": {f"M={M}": v for M, v in results.items()}}), flush=True)
 
 
+def run_kv4_decode(args):
+    """The attention side of a decode step of the 8B-class stack over the 4-bit key/value cache (32 query
+    and 8 key/value heads of 128): 64 requests with 512 to 8192 cached tokens take one token each.  One
+    step = kv4_tables once, then kv4_append and kv4_attention for each of 8 layers, replayed from a CUDA
+    graph; every layer has a cache of its own (0.32 GB read per layer, 20x L2 in all)."""
+    import torch
+
+    import int4_group_wise_b200 as q4
+
+    dev = torch.device("cuda", 0)
+    torch.cuda.set_device(dev)
+    peaks, peak_kind = load_peaks()
+    hbm = float(peaks["hbm_gbs"])
+    B, Hq, Hkv, D, P, n_layers = 64, 32, 8, 128, 64, 8
+    g = torch.Generator(device=dev)
+    g.manual_seed(0)
+    held = [512 + int(7680 * ((i * 0.6180339887) % 1.0)) for i in range(B)]
+    pages = [-(-(n + 1) // P) for n in held]
+    n_pages = sum(pages) + B
+    names = torch.randperm(n_pages, generator=g, device=dev).to(torch.int32)
+    table = torch.full((B, max(pages)), -1, dtype=torch.int32, device=dev)
+    used = 0
+    for b, n in enumerate(held):
+        c = -(-n // P)
+        table[b, :c] = names[used:used + c]
+        used += c
+    free = names[used:].contiguous()
+    lengths = torch.tensor(held, dtype=torch.int32, device=dev)
+    fresh = torch.ones(B, dtype=torch.int32, device=dev)
+    caches = []
+    for _ in range(n_layers):
+        cache = q4.kv4_cache(n_pages, P, Hkv, D, device=dev)
+        for slots in torch.arange(n_pages * P, dtype=torch.int32, device=dev).split(1 << 15):
+            x = torch.randn((2, slots.numel(), Hkv, D), generator=g, device=dev)
+            q4.kv4_append(cache, x[0], x[1], slots)
+        caches.append(cache)
+    qkv = torch.randn((n_layers, B, Hq + 2 * Hkv, D), generator=g, device=dev).bfloat16()
+    out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=dev)
+    stream = torch.cuda.Stream(dev)
+    stream.wait_stream(torch.cuda.current_stream())
+
+    def step():
+        lens, cu, slots, _ = q4.kv4_tables(lengths, fresh, table, free, P, B, stream=stream)
+        for cache, x in zip(caches, qkv):
+            q4.kv4_append(cache, x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], slots, stream=stream)
+            q4.kv4_attention(x[:, :Hq], cache, table, lens, cu, out=out, stream=stream)
+
+    for _ in range(args.warmup):
+        step()
+    stream.synchronize()
+    q4.sync_check(stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        step()
+    for _ in range(args.warmup):
+        graph.replay()
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    with ClockSampler(0) as clk:
+        with torch.cuda.stream(stream):
+            a.record(stream)
+            for _ in range(args.steps):
+                graph.replay()
+            b.record(stream)
+        torch.cuda.synchronize()
+    q4.sync_check(stream)
+    ms = a.elapsed_time(b) / args.steps
+    token = 2 * Hkv * (D // 2 + 2 * (D // 32))
+    nbytes = n_layers * ((sum(held) + B) * token + B * token + B * (2 * Hq + 2 * Hkv) * D * 2)
+    gbs = nbytes / ms / 1e6
+    print(json.dumps({
+        "metric": "4-bit key/value cache decode GB/s (tables, append, attention)", "value": gbs, "unit": "GB/s",
+        "n_gpus": 1, "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms, "higher_is_better": True,
+        "variant": "kv4-decode", "data": "synthetic", "dtype": "bf16 x int4 -> f32",
+        "config": {"workload": f"8B-class heads (32 query, 8 key/value, 128 channels), {n_layers} layers, {B} requests of "
+                               f"{min(held)}..{max(held)} tokens, pages of {P}", "l2": "inputs 20x L2 (a cache per layer)"},
+        "roofline": {"bound": "hbm", "achieved": gbs, "peak": hbm, "unit": "GB/s", "frac": gbs / hbm,
+                     "peak_kind": f"{peak_kind} copy"},
+        "us_per_layer": 1e3 * ms / n_layers, "gpu_launches": (1 + 3 * n_layers) * args.steps,
+        "clocks": clk.summary()}), flush=True)
+
+
 def run_fq_gemm(args):
     """The fake-quant forward GEMM of a QAT step on the 1B-class up-projection (W fp32 8192x2048,
     searched-range scales) for a micro-batch of --tokens tokens: TFLOP/s of the staged call
@@ -1227,11 +1309,12 @@ def main():
                          "configs 1 and 2 under stages)")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-e2e", action="store_true")
-    ap.add_argument("--variant", choices=["path", "per-channel", "w4a16-decode", "fq-gemm", "hessian-split",
-                                          "refine"],
+    ap.add_argument("--variant", choices=["path", "per-channel", "w4a16-decode", "kv4-decode", "fq-gemm",
+                                          "hessian-split", "refine"],
                     default="path",
                     help="per-channel: time the one-scale-per-row LSQ step and export instead; "
                          "w4a16-decode: time the inference GEMV on the packed 8B-class stack; "
+                         "kv4-decode: time a decode step's attention over the 4-bit key/value cache; "
                          "fq-gemm: time the fake-quant forward GEMM (staged, fused and unfused); "
                          "hessian-split: the calibration Hessian with its rows split over the ranks; "
                          "refine: one sweep of the full-objective refinement")
@@ -1254,6 +1337,8 @@ def main():
         run_per_channel(args)
     elif args.variant == "w4a16-decode":
         run_w4a16_decode(args)
+    elif args.variant == "kv4-decode":
+        run_kv4_decode(args)
     elif args.variant == "fq-gemm":
         run_fq_gemm(args)
     elif args.variant == "hessian-split":
