@@ -474,7 +474,7 @@ qat4_status qat4_kv4_gather(const qat4_kv4_cache *cache, const int32_t *slots, i
  *  Keys and values enter exactly, products are exact, sums and statistics
  *  float32; the softmax weights are rounded to bf16 for the second product
  *  (their sum is not).  The result does not depend on timing (no atomics).
- *  N >= 0; 1 <= B <= 65536; N * q_heads * head_dim <= 2^40, N * q_heads <= 2^31 - 1.
+ *  N >= 0; 1 <= B <= 65536; N * q_heads <= 2^31 - 1; max_blocks * page_size <= 2^30.
  *  With cu_q not ascending inside [0, N], rows may be computed twice or not at
  *  all; with scale * q.k overflowing float32 the row is unspecified.
  *  Errors: QAT4_ERR_NULL, _SHAPE, _ALIGN, _WORKSPACE, _CUDA; a bounded wait that

@@ -518,7 +518,7 @@ def kv4_cache(num_pages: int, page_size: int, kv_heads: int, head_dim: int, devi
 
 def _arg(t, name, dtype, shape=None):
     """Pointer of a contiguous CUDA tensor (what this refuses, _dev names)."""
-    if t.is_cuda and t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous():
+    if getattr(t, "is_cuda", False) and t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous():
         return t.data_ptr()
     return _dev(t, name, dtype, shape)
 

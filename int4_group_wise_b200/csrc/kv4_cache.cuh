@@ -19,14 +19,13 @@
 
 namespace qat4 {
 
-// mbar_wait for short waits: the clock (whose reading takes longer than most of these waits) is looked at only
-// after a few hundred polls.
-__device__ __forceinline__ bool kv4_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
-    const uint32_t b = smem_u32(bar);
-#pragma unroll 1
-    for (int i = 0; i < 256; ++i)
-        if (mbar_try_wait(b, parity)) return true;
+// mbar_wait with its loop out of line: the kernels below wait in many places, and their code is kept small.
+__device__ __noinline__ bool kv4_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
     return mbar_wait(bar, parity, abort, limit_ns);
+}
+__device__ __forceinline__ bool kv4_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+    if (mbar_try_wait(smem_u32(bar), parity)) return true;
+    return kv4_wait_slow(bar, parity, abort, limit_ns);
 }
 
 // The device's view of a cache.

@@ -179,30 +179,48 @@ struct KpItem {
 
 // Item `idx` of the grid, found by a converged warp: split, kv head, and the rank of its row tile, the
 // last (longest) tile of a request first.  Up to 32 requests are taken from the longest to the
-// shortest, so that short items even out the end; more are taken as they come.  False where there are
-// fewer tiles.
-__device__ __forceinline__ bool kp_locate(const PrefillParams& pp, int idx, int lane, KpItem& it) {
+// shortest, so that short items even out the end; more are taken 32 by 32 as they come, and `first`
+// holds the tiles before each 32 of them (`groups` entries and the total).  False where there are fewer tiles.
+constexpr int kKpGroups = 2048;                    // 32 requests each
+__device__ __noinline__ void kp_groups(const PrefillParams& pp, int* first, int groups, int lane) {
+    int sum = 0;
+    for (int g = 0; g < groups; ++g) {
+        if (lane == 0) first[g] = sum;
+        const int b = 32 * g + lane;
+        sum += __reduce_add_sync(0xffffffffu, b < pp.a.B ? kp_tiles(pp.a, kv4_request(pp.a, b)) : 0);
+    }
+    if (lane == 0) first[groups] = sum;
+    __syncwarp();
+}
+__device__ __forceinline__ bool kp_locate(const PrefillParams& pp, const int* first, int groups, int idx, int lane, KpItem& it) {
     const AttnParams& p = pp.a;
     it.split = idx % pp.splits;
     const int hr = idx / pp.splits;
     it.kvh = hr % p.c.heads;
     int rank = hr / p.c.heads;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
+    int b0 = 0;
+    if (groups > 1) {
+        if (rank >= first[groups]) return false;
+        int lo = 0, hi = groups;                                   // first[lo] <= rank < first[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (first[mid] <= rank) lo = mid; else hi = mid;
+        }
+        b0 = 32 * lo;
+        rank -= first[lo];
+    }
+    {
         const int b = b0 + lane;
         Request r = {0, 0, 0, 0, 0};
         if (b < p.B) r = kv4_request(p, b);
         const int n = b < p.B ? kp_tiles(p, r) : 0;
-        int before = 0, all = 0;                                   // tiles of the requests that come first, of all
+        int before = 0;                                            // tiles of the requests that come first
         for (int j = 0; j < 32 && b0 + j < p.B; ++j) {
             const int nj = __shfl_sync(0xffffffffu, n, j), lj = __shfl_sync(0xffffffffu, r.len, j);
-            if (p.B <= 32 ? lj > r.len || (lj == r.len && j < lane) : j < lane) before += nj;
-            all += nj;
+            if (lj > r.len || (lj == r.len && j < lane)) before += nj;
         }
         const uint32_t hit = __ballot_sync(0xffffffffu, rank >= before && rank < before + n);
-        if (hit == 0) {
-            rank -= all;
-            continue;
-        }
+        if (hit == 0) return false;
         const int src = __ffs(hit) - 1;
         const int tile = n - 1 - (rank - before);                  // right in lane src
         it.state = 1;
@@ -223,7 +241,6 @@ __device__ __forceinline__ bool kp_locate(const PrefillParams& pp, int idx, int 
         it.t_first = (blk0 + j0) * kKpBlock;
         return true;
     }
-    return false;
 }
 
 template <int D>
@@ -237,6 +254,7 @@ kv4_prefill_kernel(const PrefillParams pp) {
     __shared__ __align__(8) uint64_t s_full[2][2], p_full[2][2], o_full[2][2];     // [tile][buffer]
     __shared__ __align__(8) uint64_t q_full[2], item_full, item_free, clc_bar, done_bar[2];
     __shared__ KpItem s_item;
+    __shared__ int s_first[kKpGroups + 1];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
 
@@ -278,7 +296,7 @@ kv4_prefill_kernel(const PrefillParams pp) {
     const int page = p.c.page, sh = __ffs(page) - 1;
     // waits of a converged warp: all lanes go on, or none
     auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1u, abort, limit));
+        return __all_sync(0xffffffffu, kv4_wait(bar, phase & 1u, abort, limit));
     };
     // The next item (k counts them); `release`: give the slot back at once.
     auto next_item = [&](KpItem& it, uint32_t k, bool release) -> bool {
@@ -611,12 +629,14 @@ kv4_prefill_kernel(const PrefillParams pp) {
             mbar_wait(&done_bar[x], 0, nullptr, kDrainLimitNs);
         } else if (warp == 14) {
             // ---------------------------------------------------------- the items
+            const int groups = (p.B + 31) / 32;
+            if (groups > 1) kp_groups(pp, s_first, groups, lane);
             int idx = static_cast<int>(blockIdx.x);
             uint32_t k = 0, asked = 0;
             bool ok = true, more = true;
             while (ok) {
                 KpItem it;
-                const bool work = more && kp_locate(pp, idx, lane, it);
+                const bool work = more && kp_locate(pp, s_first, groups, idx, lane, it);
                 if (work || !more) {
                     if (k > 0) ok = wait(&item_free, k - 1);           // everyone has read the item before
                     if (!ok) break;

@@ -1099,7 +1099,8 @@ extern "C" size_t qat4_kv4_attention_workspace_bytes(int64_t N, int64_t B, int64
                                                      int64_t head_dim, int32_t page_size, int64_t max_blocks) {
     const int64_t top = (int64_t(1) << 31) - 1;
     if (N < 0 || B < 1 || B > 65536 || q_heads < 1 || q_heads > 65536 || kv_heads < 1 || q_heads % kv_heads != 0 ||
-        (head_dim != 64 && head_dim != 128) || N > top / q_heads || page_size < 1 || max_blocks < 1 || max_blocks > top)
+        (head_dim != 64 && head_dim != 128) || N > top / q_heads || page_size < 1 || page_size > 128 || max_blocks < 1 ||
+        max_blocks > (int64_t(1) << 30) / page_size)
         return 0;
     const int64_t group = q_heads / kv_heads;
     const Kv4Plan pl = kv4_plan(N, B, group, kv_heads);
@@ -1151,7 +1152,7 @@ qat4_status qat4_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t N, i
     if (!block_table || !seq_lens || !cu_q || (N != 0 && (!q || !out))) return QAT4_ERR_NULL;
     const int64_t top = (int64_t(1) << 31) - 1, D = cache->head_dim, H = cache->kv_heads;
     if (N < 0 || B < 1 || B > 65536 || q_heads < 1 || q_heads % H != 0 || q_heads / H > 64 || q_heads > 65536 ||
-        N > top / q_heads || N * q_heads / H / qat4::kKpRows + B > top / (16 * H) || q_stride < q_heads * D || q_stride > top || max_blocks < 1 || max_blocks > top ||
+        N > top / q_heads || N * q_heads / H / qat4::kKpRows + B > top / (16 * H) || q_stride < q_heads * D || q_stride > top || max_blocks < 1 || max_blocks > (int64_t(1) << 30) / cache->page_size ||
         table_stride < max_blocks || table_stride > (int64_t(1) << 40) || !(scale > 0.0f) || !std::isfinite(scale) ||
         !std::isfinite(scale * 1.4426950408889634f) || (causal != 0 && causal != 1) || window < 0 ||
         (window > 0 && !causal))
@@ -1184,7 +1185,7 @@ qat4_status qat4_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t N, i
     p.group = static_cast<int>(q_heads / H);
     p.max_blocks = static_cast<int>(max_blocks);
     p.causal = causal;
-    p.window = window;
+    p.window = std::min(window, int32_t(1) << 30);      // a request has at most 2^30 tokens: no limit either way
     p.scale_log2 = scale * 1.4426950408889634f;
     // generous bound of a wait: 10 s, and 20 us for every 128 tokens that the table can name (the longest wait of
     // a warp is for another tile's item, one or two microseconds per 128 tokens)

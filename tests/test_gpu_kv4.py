@@ -297,6 +297,27 @@ def test_attention_prompt_on_long_context():
     _check(*_batch([3001], [129], 16, 1, 64, 2, seed=2), window=700)
 
 
+def test_attention_many_prompts():
+    """More requests of many rows than a warp has lanes, and groups of 32 of them without any."""
+    rng = np.random.default_rng(5)
+    lens = rng.integers(1, 300, 75).tolist()
+    nqs = [int(rng.integers(1, n + 1)) for n in lens]
+    _check(*_batch(lens, nqs, 16, 1, 64, 4, seed=3))
+    lens = [40] * 70 + [200, 130] + [1] * 90
+    nqs = [0] * 70 + [200, 90] + [1] * 90
+    _check(*_batch(lens, nqs, 64, 2, 128, 64, seed=4))
+
+
+def test_attention_window_of_any_size():
+    """A window near 2^31 is no window, for requests with more queries than tokens too."""
+    for nqs in ([5, 1], [200, 90]):
+        a = _batch([3, 300], nqs, 16, 1, 64, 4, seed=2)
+        want = _run(*a)
+        for window in (2 ** 31 - 1, 2 ** 40):
+            got = _run(*a, window=window)
+            assert torch.equal(got[0].view(torch.int16), want[0].view(torch.int16)) and torch.equal(got[1], want[1])
+
+
 def test_attention_large_and_small_scores():
     """Scores that leave one key all the weight, equal scores, and a scale other than 1/sqrt(D)."""
     q, cache, table, lens, cu = _batch([300, 129, 700], [1, 20, 300], 64, 1, 128, 4, seed=6)

@@ -88,7 +88,8 @@ def test_attention_validation():
         assert f(**kw) == 1, kw
     for kw in (dict(N=-1), dict(B=0), dict(B=65537), dict(Hq=5), dict(Hq=0), dict(Hq=130, qs=130 * 64), dict(qs=248),
                dict(mb=0), dict(ts=799), dict(scale=0.0), dict(scale=-0.5), dict(scale=math.nan), dict(scale=math.inf),
-               dict(scale=3e38), dict(causal=2), dict(window=-1), dict(window=3, causal=0), dict(N=1 << 30)):
+               dict(scale=3e38), dict(causal=2), dict(window=-1), dict(window=3, causal=0), dict(N=1 << 30),
+               dict(mb=(1 << 26) + 1, ts=1 << 27)):
         assert f(**kw) == 2, kw
     for kw in (dict(q=MIS4), dict(qs=260), dict(out=MIS4), dict(ws=MIS4), dict(t=MIS1), dict(lse=MIS1), dict(cu=MIS1)):
         assert f(**kw) == 3, kw
