@@ -6,8 +6,8 @@
 //
 // Rows.  The group = q_heads / kv_heads query heads that share a key/value head
 // are packed with the request's query tokens into rows (token * group + head),
-// so a cached token is read and decoded once for all rows of a tile (4, 8 or
-// 16).
+// so a cached token is read and decoded once for all rows of a tile (4, 8, 16
+// or 24).
 //
 // Bound: HBM.  A cached token of a head costs 2 * (D/2 + D/16) bytes (144 at
 // D = 128) and 4 * D * rows flop, far below the tensor cores' balance, so the
@@ -149,11 +149,15 @@ struct KaLayout {
     static constexpr int kCodes = kKaChunk * D / 2;
     static constexpr int kSteps = kKaChunk * (D / 32) * 2;
     static constexpr int kStage = 2 * kCodes + 2 * kSteps;
-    static constexpr int kPerSm = ROWS == 16 ? 2 : 3;             // CTAs per SM (registers, shared memory)
-    static constexpr int kStages = kPerSm == 3 ? 3 : 4;           // 55 or 73 KB of ring at D = 128
+    static constexpr int kN = (ROWS + 7) / 8;                     // MMA column tiles of 8 rows
+    static constexpr bool kQShared = ROWS == 24;                  // q in shared memory, where registers run out
+    static constexpr int kPass = kQShared && D == 128 ? 1 : 2;    // tiles of 16 tokens of a warp at once
+    static constexpr int kPerSm = ROWS >= 16 ? 2 : 3;             // CTAs per SM (registers, shared memory)
+    static constexpr int kStages = ROWS == 16 ? 4 : 3;            // 73 or 55 KB of ring at D = 128
     static constexpr int kORow = D * 4 + 16;                      // bytes of an output row in the join buffer
     static constexpr int kJoin = kKaWarps * ROWS * kORow;
-    static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStage + kJoin;
+    static constexpr int kQ = kQShared ? kN * (D / 16) * 32 * 8 : 0;
+    static constexpr size_t kSmem = static_cast<size_t>(kStages) * kStage + kJoin + kQ;
 };
 
 // Workspace floats of one piece: ROWS rows of D outputs, then ROWS maxima (log2) and ROWS sums.
@@ -223,14 +227,16 @@ kv4_decode_kernel(const AttnParams p) {
     using L = KaLayout<D, ROWS>;
     constexpr int kStages = L::kStages;
     constexpr bool kLo = ROWS == 4;            // columns 4..7 carry the weights' rounding remainders
-    constexpr int kN = ROWS == 16 ? 2 : 1;     // MMA column tiles of 8 rows
+    constexpr int kN = L::kN;
+    constexpr bool kQs = L::kQShared;
+    constexpr int kPass = L::kPass;
     constexpr int kW = D / 32;                 // words of a thread's key channels (4 or 2)
     constexpr int kVW = D / 64;                // words of a thread's value channels (2 or 1)
     constexpr int kM = D / 16;                 // output tiles of 16 channels
     extern __shared__ __align__(128) uint8_t ka_smem[];
     __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages];
     __shared__ uint32_t live_bits[kStages][4];
-    __shared__ float join_m[kKaWarps][16], join_l[kKaWarps][16];
+    __shared__ float join_m[kKaWarps][24], join_l[kKaWarps][24];
     __shared__ __align__(16) float res[CL ? ka_piece<D, ROWS>() : 4];
     __shared__ int64_t scan[32], s_skip;
     __shared__ int s_b;
@@ -378,7 +384,8 @@ kv4_decode_kernel(const AttnParams p) {
         // ---------------------------------------------------------- consumers
         const int g = lane >> 2, t = lane & 3;
         const float c = p.scale_log2;
-        uint32_t qb[kN][2 * kW][2];                 // q of row 8n + g, this thread's channels, operand order
+        uint32_t qb[kQs ? 1 : kN][2 * kW][2];       // q of row 8n + g, this thread's channels, operand order
+        const uint32_t qs = ring + kStages * L::kStage + L::kJoin + 8u * lane;     // the same in shared memory
         float acc[kM][kN][4];
         float m[kN][2], l[kN][2];                   // of rows 8n + 2t and 8n + 2t + 1: reference maximum, sum
         int lim[kN][2], low[kN][2];                 // these rows see the tokens low..lim
@@ -401,12 +408,21 @@ kv4_decode_kernel(const AttnParams p) {
                                           static_cast<int64_t>(at.kvh * p.group + (in ? row - tok * p.group : 0)) * D + 8 * kW * t;
 #pragma unroll
                     for (int w = 0; w < kW; ++w) {
+                        if (kQs && (n * kW + w) % kKaWarps != warp) continue;        // the warps share this work
                         uint4 x = make_uint4(0u, 0u, 0u, 0u);
                         if (in) x = __ldg(reinterpret_cast<const uint4*>(src) + w);
-                        qb[n][2 * w][0] = __byte_perm(x.x, x.z, 0x5410);
-                        qb[n][2 * w][1] = __byte_perm(x.x, x.z, 0x7632);
-                        qb[n][2 * w + 1][0] = __byte_perm(x.y, x.w, 0x5410);
-                        qb[n][2 * w + 1][1] = __byte_perm(x.y, x.w, 0x7632);
+                        const uint32_t y[4] = {__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                                               __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632)};
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (kQs) {
+                                asm volatile("st.shared.v2.b32 [%0], {%1, %2};"
+                                             :: "r"(qs + 256u * (n * 2 * kW + 2 * w + i)), "r"(y[2 * i]), "r"(y[2 * i + 1]) : "memory");
+                            } else {
+                                qb[kQs ? 0 : n][2 * w + i][0] = y[2 * i];
+                                qb[kQs ? 0 : n][2 * w + i][1] = y[2 * i + 1];
+                            }
+                        }
                     }
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -424,6 +440,7 @@ kv4_decode_kernel(const AttnParams p) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) acc[i][n][j] = 0.0f;
                 }
+                if (kQs) asm volatile("bar.sync 1, %0;" :: "n"(32 * kKaWarps) : "memory");
                 seg_c0 = at.ch;
                 fresh = false;
             }
@@ -433,23 +450,26 @@ kv4_decode_kernel(const AttnParams p) {
                 const uint32_t sb = ring + s * L::kStage;
                 const uint32_t live = live_bits[s][warp];
                 const int t0 = at.t0() + 32 * warp;                  // first token of this warp's 32
-                // ---- S^T = K Q^T, two tiles of 16 tokens
-                float sv[2][kN][4];
+                // 32 tokens at once, 16 where registers run out
+#pragma unroll 1
+                for (int k0 = 0; k0 < 2; k0 += kPass) {
+                // ---- S^T = K Q^T, tiles of 16 tokens
+                float sv[kPass][kN][4];
                 const uint32_t kbase = sb + (32 * warp + g) * (D / 2) + 4 * kW * t;
                 const uint32_t sbase = sb + 2 * L::kCodes + (32 * warp + g) * (D / 32) * 2 + 2 * (t * kW / 4);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                for (int k = 0; k < kPass; ++k) {
                     uint32_t w[2][kW], s2[2], o2[2];                 // tokens g and g + 8 of the tile
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (kW == 4) {
-                            const uint4 x = gm_lds128(kbase + (16 * k + 8 * h) * (D / 2));
+                            const uint4 x = gm_lds128(kbase + (16 * (k0 + k) + 8 * h) * (D / 2));
                             w[h][0] = x.x; w[h][1] = x.y; w[h][2 % kW] = x.z; w[h][3 % kW] = x.w;
                         } else {
-                            const uint2 x = lds64(kbase + (16 * k + 8 * h) * (D / 2));
+                            const uint2 x = lds64(kbase + (16 * (k0 + k) + 8 * h) * (D / 2));
                             w[h][0] = x.x; w[h][1] = x.y;
                         }
-                        s2[h] = __byte_perm(lds_u16(sbase + (16 * k + 8 * h) * (D / 32) * 2), 0u, 0x1010);
+                        s2[h] = __byte_perm(lds_u16(sbase + (16 * (k0 + k) + 8 * h) * (D / 32) * 2), 0u, 0x1010);
                         o2[h] = kv4_off(s2[h]);
                     }
 #pragma unroll
@@ -464,9 +484,18 @@ kv4_decode_kernel(const AttnParams p) {
                         }
 #pragma unroll
                         for (int n = 0; n < kN; ++n) {
-                            if (i == 0) ka_mma0(sv[k][n], a[0][0], a[0][1], a[0][2], a[0][3], qb[n][0][0], qb[n][0][1]);
-                            else gm_mma(sv[k][n], a[0][0], a[0][1], a[0][2], a[0][3], qb[n][2 * i][0], qb[n][2 * i][1]);
-                            gm_mma(sv[k][n], a[1][0], a[1][1], a[1][2], a[1][3], qb[n][2 * i + 1][0], qb[n][2 * i + 1][1]);
+                            uint2 q0, q1;
+                            if (kQs) {
+                                q0 = lds64(qs + 256u * (n * 2 * kW + 2 * i));
+                                q1 = lds64(qs + 256u * (n * 2 * kW + 2 * i + 1));
+                            } else {
+                                const uint32_t (&y)[2 * kW][2] = qb[kQs ? 0 : n];
+                                q0 = make_uint2(y[2 * i][0], y[2 * i][1]);
+                                q1 = make_uint2(y[2 * i + 1][0], y[2 * i + 1][1]);
+                            }
+                            if (i == 0) ka_mma0(sv[k][n], a[0][0], a[0][1], a[0][2], a[0][3], q0.x, q0.y);
+                            else gm_mma(sv[k][n], a[0][0], a[0][1], a[0][2], a[0][3], q0.x, q0.y);
+                            gm_mma(sv[k][n], a[1][0], a[1][1], a[1][2], a[1][3], q1.x, q1.y);
                         }
                     }
                 }
@@ -477,12 +506,12 @@ kv4_decode_kernel(const AttnParams p) {
                     plain = plain && min(lim[n][0], lim[n][1]) >= t0 + 31 && max(low[n][0], low[n][1]) <= t0;
                 if (!__all_sync(0xffffffffu, plain)) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
+                    for (int k = 0; k < kPass; ++k)
 #pragma unroll
                         for (int n = 0; n < kN; ++n)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const int off = 16 * k + g + 8 * (i >> 1), tk = t0 + off;
+                                const int off = 16 * (k0 + k) + g + 8 * (i >> 1), tk = t0 + off;
                                 if (!((live >> off) & 1u) || tk > lim[n][i & 1] || tk < low[n][i & 1]) sv[k][n][i] = -INFINITY;
                             }
                 }
@@ -493,7 +522,9 @@ kv4_decode_kernel(const AttnParams p) {
                 for (int n = 0; n < kN; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        x[n][e] = fmaxf(fmaxf(sv[0][n][e], sv[0][n][2 + e]), fmaxf(sv[1][n][e], sv[1][n][2 + e])) * c;
+                        float y = fmaxf(sv[0][n][e], sv[0][n][2 + e]);
+                        if (kPass == 2) y = fmaxf(y, fmaxf(sv[kPass - 1][n][e], sv[kPass - 1][n][2 + e]));
+                        x[n][e] = y * c;
                         grow = grow || x[n][e] > m[n][e] + kKaGrow;
                     }
                 if (__any_sync(0xffffffffu, grow)) {
@@ -520,12 +551,12 @@ kv4_decode_kernel(const AttnParams p) {
                         }
                 }
                 // ---- P, transposed into the second product's operand
-                uint32_t pb[2][kN][2];
+                uint32_t pb[kPass][kN][2];
 #pragma unroll
                 for (int n = 0; n < kN; ++n) {
                     const float n0 = m[n][0] == -INFINITY ? 0.0f : -m[n][0], n1 = m[n][1] == -INFINITY ? 0.0f : -m[n][1];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
+                    for (int k = 0; k < kPass; ++k)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const float e0 = ex2(fmaf(sv[k][n][2 * h], c, n0)), e1 = ex2(fmaf(sv[k][n][2 * h + 1], c, n1));
@@ -542,11 +573,11 @@ kv4_decode_kernel(const AttnParams p) {
                 }
                 // ---- O^T += V^T P^T
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                for (int k = 0; k < kPass; ++k) {
                     uint32_t v[2][8 * kVW];                  // pairs of tokens (2t, 2t+1) and (2t+8, 2t+9)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int off = 16 * k + 8 * h + 2 * t;
+                        const int off = 16 * (k0 + k) + 8 * h + 2 * t;
                         const uint32_t vb = sb + L::kCodes + (32 * warp + off) * (D / 2) + 4 * kVW * g;
                         const uint32_t ss = sb + 2 * L::kCodes + L::kSteps + (32 * warp + off) * (D / 32) * 2 + 2 * (kVW * g / 4);
                         uint32_t wa[kVW], wb[kVW];
@@ -581,6 +612,7 @@ kv4_decode_kernel(const AttnParams p) {
 #pragma unroll
                         for (int n = 0; n < kN; ++n)
                             gm_mma(acc[i][n], v[0][i], v[0][kM + i], v[1][i], v[1][kM + i], pb[k][n][0], pb[k][n][1]);
+                }
                 }
             }
             // the slot is released only once what was loaded from it has been used

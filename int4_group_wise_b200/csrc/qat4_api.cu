@@ -934,8 +934,9 @@ static bool kv4_attrs(DeviceInfo* info) {
     std::lock_guard<std::mutex> lock(g_mutex);
     if (info->kv4_attr) return true;
     if (!smem_attr(qat4::kv4_tables_kernel, qat4::tables_smem_bytes(qat4::kTbMaxRequests))) return false;
-    if (!kv4_decode_attr<64, 4>() || !kv4_decode_attr<64, 8>() || !kv4_decode_attr<64, 16>() ||
-        !kv4_decode_attr<128, 4>() || !kv4_decode_attr<128, 8>() || !kv4_decode_attr<128, 16>())
+    if (!kv4_decode_attr<64, 4>() || !kv4_decode_attr<64, 8>() || !kv4_decode_attr<64, 16>() || !kv4_decode_attr<64, 24>() ||
+        !kv4_decode_attr<128, 4>() || !kv4_decode_attr<128, 8>() || !kv4_decode_attr<128, 16>() ||
+        !kv4_decode_attr<128, 24>())
         return false;
     if (!smem_attr(qat4::kv4_prefill_kernel<64>, qat4::KpLayout<64>::kSmem) ||
         !smem_attr(qat4::kv4_prefill_kernel<128>, qat4::KpLayout<128>::kSmem))
@@ -1051,8 +1052,8 @@ static constexpr int kKaGrid = 3 * kKaSms;       // most CTAs of the decode kern
 //   more, and one request: the prefill kernel takes it;
 //   more, and several: requests of up to kRowsDecode rows go to the decode kernel, the others to the prefill
 //   kernel.
-// 16 requests of 700..6007 tokens, 32/8 heads of 128: 20 rows each take 64 us in the decode kernel and 68 in the
-// other, 36 rows 97 and 69.
+// 16 requests of 700..6007 tokens, 32/8 heads of 128: 20 rows each take 57 us in the decode kernel and 68 in the
+// other, 36 rows 97 and 68.
 static constexpr int64_t kRowsDecode = 32;
 struct Kv4Plan {
     bool decode, prefill;
@@ -1078,11 +1079,16 @@ static Kv4Plan kv4_plan(int64_t N, int64_t B, int64_t group, int64_t kv_heads) {
 }
 
 static size_t kv4_decode_bytes(int64_t D) {
-    return static_cast<size_t>(kKaGrid) * 2 * (16 + 16 * (static_cast<size_t>(D) + 2) * 4);
+    return static_cast<size_t>(kKaGrid) * 2 * (16 + 24 * (static_cast<size_t>(D) + 2) * 4);
 }
 
-// Rows of the decode kernel's tiles: as tall as the average request's.
-static int kv4_tile_rows(int64_t rows, int64_t B) { return rows <= 4 * B ? 4 : rows <= 8 * B ? 8 : 16; }
+// Rows of the decode kernel's tiles: as tall as the average request's, which then reads its tokens once.  From 17
+// to 24 rows that pays once there are tiles enough to fill the GPU (5 drafted tokens, 32/8 heads of 128: 16
+// requests take 57 us with tiles of 24 rows and 65 with two of 16; four requests 29 and 25); above, a request
+// takes two tiles in any case, and tiles of 16 have the faster kernel.
+static int kv4_tile_rows(int64_t rows, int64_t B, int64_t kv_heads) {
+    return rows <= 4 * B ? 4 : rows <= 8 * B ? 8 : rows > 16 * B && rows <= 24 * B && B * kv_heads >= 64 ? 24 : 16;
+}
 
 // Clusters of the one-launch form of the decode kernel (upper bound of the row tiles over all kv heads), or 0
 // where the batch fills the GPU, or a request may be longer than four chunks for each CTA of a cluster (one
@@ -1091,7 +1097,7 @@ static int kv4_tile_rows(int64_t rows, int64_t B) { return rows <= 4 * B ? 4 : r
 static int64_t kv4_clusters(int64_t N, int64_t B, int64_t group, int64_t kv_heads, int64_t page, int64_t max_blocks) {
     const int64_t rows = N * group, chunk = qat4::kKaChunk;
     if ((max_blocks * page + chunk - 1) / chunk > 4 * qat4::kKaCluster) return 0;
-    const int64_t tiles = (rows / kv4_tile_rows(rows, B) + std::min(B, rows)) * kv_heads;
+    const int64_t tiles = (rows / kv4_tile_rows(rows, B, kv_heads) + std::min(B, rows)) * kv_heads;
     return tiles * qat4::kKaCluster <= 2 * kKaSms ? tiles : 0;
 }
 
@@ -1124,10 +1130,11 @@ static bool kv4_decode_launch(const qat4::AttnParams& p, int64_t clusters, cudaS
 
 template <int D>
 static bool kv4_decode_rows(const qat4::AttnParams& p, int64_t clusters, cudaStream_t stream) {
-    const int rows = kv4_tile_rows(static_cast<int64_t>(p.N) * p.group, p.B);
+    const int rows = kv4_tile_rows(static_cast<int64_t>(p.N) * p.group, p.B, p.c.heads);
     return rows == 4 ? kv4_decode_launch<D, 4>(p, clusters, stream)
          : rows == 8 ? kv4_decode_launch<D, 8>(p, clusters, stream)
-                     : kv4_decode_launch<D, 16>(p, clusters, stream);
+         : rows == 16 ? kv4_decode_launch<D, 16>(p, clusters, stream)
+                      : kv4_decode_launch<D, 24>(p, clusters, stream);
 }
 
 template <int D>

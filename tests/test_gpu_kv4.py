@@ -297,6 +297,21 @@ def test_attention_prompt_on_long_context():
     _check(*_batch([3001], [129], 16, 1, 64, 2, seed=2), window=700)
 
 
+@pytest.mark.parametrize("dim,new,q_heads,heads", [(64, 5, 8, 2), (128, 5, 8, 2), (64, 3, 7, 1), (128, 20, 1, 1),
+                                                   (128, 1, 17, 1), (64, 1, 24, 1)])
+def test_attention_drafts(dim, new, q_heads, heads):
+    """17 to 24 rows per request and kv head, requests enough for tiles of 24 rows; one request with more, one
+    with none."""
+    rng = np.random.default_rng(dim + new)
+    B = 70 // heads
+    lens = rng.integers(new, 400, B).tolist()
+    nqs = [new] * B
+    nqs[3], nqs[5], nqs[7] = 0, 2 * new, max(0, new - 2)
+    lens[0], lens[5] = 1500, 2 * new
+    _check(*_batch(lens, nqs, 32, heads, dim, q_heads, seed=dim + q_heads))
+    _check(*_batch(lens, nqs, 16, heads, dim, q_heads, seed=dim + q_heads + 1), window=100)
+
+
 def test_attention_many_prompts():
     """More requests of many rows than a warp has lanes, and groups of 32 of them without any."""
     rng = np.random.default_rng(5)
