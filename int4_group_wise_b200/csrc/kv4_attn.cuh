@@ -37,8 +37,9 @@
 // workspace, and kv4_combine_kernel joins them in order (no atomics: the result
 // does not depend on timing).
 //
-// Data movement.  A producer warp streams each unit's pages with untiled bulk
-// copies into a ring (one copy per page and array: a page's head is contiguous)
+// Data movement.  A producer warp streams each unit's pages into a ring, the
+// codes with untiled bulk copies (one per page: a page's head is contiguous),
+// the steps with 16-byte copies of its lanes,
 // and writes which of the 128 tokens exist: tokens past the length, of pages
 // that the table does not name, or that no query of the request can see any
 // more are never attended to, and their steps are taken as 0, whatever bytes
@@ -266,7 +267,7 @@ kv4_decode_kernel(const AttnParams p) {
         s_b = -1;
         abort_flag = 0;
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full_bar[s], 1);
+            mbar_init(&full_bar[s], 33);            // the producer's codes, and each of its lanes' steps
             mbar_init(&empty_bar[s], kKaWarps);
         }
         fence_mbar_init();
@@ -322,13 +323,9 @@ kv4_decode_kernel(const AttnParams p) {
     if (warp == kKaWarps) {
         // ------------------------------------------------------------ producer
         const int np = kKaChunk >> sh;                         // pages per chunk, 1..8
-        const int arr = lane / np, pi = lane - arr * np;       // lane's array and page
-        const bool has = lane < 4 * np;
-        const int unit = (arr & 1) ? (D / 32) * 2 : D / 2;     // bytes per token of the array
-        const uint8_t* base = arr == 0 ? p.c.kc : arr == 1 ? reinterpret_cast<const uint8_t*>(p.c.ks)
-                            : arr == 2 ? p.c.vc : reinterpret_cast<const uint8_t*>(p.c.vs);
-        const uint32_t dst0 = (arr == 0 ? 0 : arr == 1 ? 2 * L::kCodes : arr == 2 ? L::kCodes : 2 * L::kCodes + L::kSteps) +
-                              pi * page * unit;
+        const bool vals = lane >= np, has = lane < 2 * np;     // lane's page of the key codes, then of the value codes
+        const int pi = vals ? lane - np : lane;
+        const uint32_t dst0 = (vals ? L::kCodes : 0) + pi * page * (D / 2);
         // this lane's entry of the block table for a unit, -1 where nothing is to be copied; loaded one unit
         // ahead, so that its latency is not part of the ring's round trip
         auto entry = [&](const Place<ROWS>& x) -> int {
@@ -350,7 +347,7 @@ kv4_decode_kernel(const AttnParams p) {
             if (id >= p.c.pages) id = -1;
             const int t0 = at.t0(), pt = t0 + pi * page;
             // tokens that exist, 32 per word in lanes 0..3: inside [lo, len) and of a page that exists
-            const uint32_t ids = __ballot_sync(0xffffffffu, arr == 0 && id >= 0);
+            const uint32_t ids = __ballot_sync(0xffffffffu, !vals && id >= 0);
             if (lane < 4) {
                 const int w0 = t0 + 32 * lane;
                 const int e = min(max(at.r.len - w0, 0), 32), f = min(max(at.r.lo - w0, 0), 32);
@@ -360,22 +357,38 @@ kv4_decode_kernel(const AttnParams p) {
                                 : ((pg & 1u) ? 0xffffu : 0u) | ((pg & 2u) ? 0xffff0000u : 0u);
                 live_bits[s][lane] = m;
             }
-            // whole multiples of 4 tokens, so that every copy is a multiple of 16 bytes
+            // codes: bulk copies, whole multiples of 4 tokens (16 bytes and more)
             const int ntok = min(page, (at.r.len - pt + 3) & ~3);
-            const uint32_t bytes = id >= 0 ? static_cast<uint32_t>(ntok * unit) : 0u;
+            const uint32_t bytes = has && id >= 0 ? static_cast<uint32_t>(ntok) * (D / 2) : 0u;
             const uint32_t sum = __reduce_add_sync(0xffffffffu, bytes);
             __syncwarp();
             if (lane == 0) mbar_arrive_expect_tx(&full_bar[s], sum);
             __syncwarp();
             if (bytes > 0)
                 bulk_load(ka_smem + s * L::kStage + dst0,
-                          base + ((static_cast<int64_t>(id) * p.c.heads + at.kvh) * page) * unit, bytes, &full_bar[s]);
+                          (vals ? p.c.vc : p.c.kc) + ((static_cast<int64_t>(id) * p.c.heads + at.kvh) * page) * (D / 2), bytes,
+                          &full_bar[s]);
+            // steps: 16-byte copies by every lane, whatever the page size (a bulk copy of a 16-token page's 64 or
+            // 128 bytes would cost as much as one of its codes)
+#pragma unroll
+            for (int i = 0; i < L::kSteps / 512; ++i) {
+                const int token = (lane + 32 * i) * (16 / (D / 16));
+                const int from = __shfl_sync(0xffffffffu, id, token >> sh);
+                if (from >= 0) {
+                    const int64_t src = ((static_cast<int64_t>(from) * p.c.heads + at.kvh) * page + (token & (page - 1))) * (D / 32);
+                    const uint32_t dst = ring + s * L::kStage + 2 * L::kCodes + 16u * (lane + 32 * i);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(p.c.ks + src) : "memory");
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst + L::kSteps), "l"(p.c.vs + src) : "memory");
+                }
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(&full_bar[s])) : "memory");
             issued = u - u0 + 1;
             if (++s == kStages) { s = 0; ph ^= 1u; }
             at = ahead;
             id = id_next;
         }
         // no copy may still be landing when the CTA exits
+        asm volatile("cp.async.wait_all;" ::: "memory");
         if (lane == 0)
             for (int64_t i = (issued > kStages ? issued - kStages : 0); i < issued; ++i)
                 mbar_wait(&full_bar[i % kStages], static_cast<uint32_t>(i / kStages) & 1u, nullptr, kDrainLimitNs);
