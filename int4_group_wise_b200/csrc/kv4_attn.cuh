@@ -124,9 +124,18 @@ struct Place {
         b = b_;
         r = kv4_request(p, b);
         un = kv4_units<ROWS>(p, r);
-        ch = static_cast<int>(skip % un.chunks);
-        tile = static_cast<int>((skip / un.chunks) % un.tiles);
-        kvh = static_cast<int>(skip / (static_cast<int64_t>(un.chunks) * un.tiles));
+        // 64-bit divisions only where a request has that many units
+        if (skip <= 0x7fffffff) {
+            const uint32_t s = static_cast<uint32_t>(skip), t = s / static_cast<uint32_t>(un.chunks);
+            ch = static_cast<int>(s - t * un.chunks);
+            kvh = static_cast<int>(t / static_cast<uint32_t>(un.tiles));
+            tile = static_cast<int>(t - kvh * un.tiles);
+        } else {
+            const int64_t t = skip / un.chunks;
+            ch = static_cast<int>(skip - t * un.chunks);
+            kvh = static_cast<int>(t / un.tiles);
+            tile = static_cast<int>(t - static_cast<int64_t>(kvh) * un.tiles);
+        }
     }
     // the next unit; `more`: there is one
     __device__ __forceinline__ void next(const AttnParams& p, bool more) {
@@ -285,8 +294,12 @@ kv4_decode_kernel(const AttnParams p) {
         u1 = u0 < total ? u0 + 1 : u0;
     } else {
         const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);     // every CTA of these has work
-        u0 = blockIdx.x < ctas ? total * blockIdx.x / ctas : 0;
-        u1 = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : 0;
+        // range i starts at floor(total i / ctas), without 64-bit divisions while there are few units
+        const uint32_t n = max(1u, static_cast<uint32_t>(ctas)), i = blockIdx.x;
+        const int64_t each = total <= 0x7fffffff ? static_cast<uint32_t>(total) / n : total / n;
+        const uint32_t more = static_cast<uint32_t>(total - each * n);
+        u0 = i < ctas ? each * i + more * i / n : 0;
+        u1 = i < ctas ? each * (i + 1) + more * (i + 1) / n : 0;
     }
     if (u0 < u1 && u0 >= before && u0 < before + mine) {
         int64_t at = before;

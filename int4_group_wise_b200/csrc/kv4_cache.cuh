@@ -220,12 +220,14 @@ __device__ __forceinline__ float kv4_quotient(float a, float d, float r) {
     const float q0 = __fmul_rn(a, r);
     return __fmaf_rn(__fmaf_rn(-q0, d, a), r, q0);
 }
-__device__ __forceinline__ uint32_t kv4_pack8(const float (&v)[8], float m, float& step) {
+__device__ __forceinline__ float kv4_step_fast(float m, float& r) {
     const float d = kv4_quotient(m, 7.0f, 1.0f / 7.0f);
     const float up = __uint_as_float((__float_as_uint(d) + 0x7FFFFu) & ~0x7FFFFu);
-    step = d < 0x1p-100f ? 0.0f : fminf(up, 0x1p100f);
-    float r;
+    const float step = d < 0x1p-100f ? 0.0f : fminf(up, 0x1p100f);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(step));
+    return step;
+}
+__device__ __forceinline__ uint32_t kv4_pack8(const float (&v)[8], float step, float r) {
     uint32_t w = 0;
 #pragma unroll
     for (int i = 7; i >= 0; --i) {
@@ -237,9 +239,9 @@ __device__ __forceinline__ uint32_t kv4_pack8(const float (&v)[8], float m, floa
 }
 
 constexpr int kKvBlock = 256;
-constexpr int kKvItems = 4;                        // 8-channel words per thread of large batches, loaded together
+constexpr int kKvItems = 4;                        // gather: 8-channel words per thread of large batches, loaded together
 
-// How blocks cover the words of n tokens of k (blockIdx.y = 0) or v (1): `tokens` whole tokens per block, or
+// How blocks cover the words (or pairs of words) of n tokens of k (blockIdx.y = 0) or v (1): `tokens` whole tokens per block, or
 // one token in `parts` blocks when it has more words than a block takes.
 struct Kv4Span {
     int64_t n;
@@ -255,43 +257,42 @@ __device__ __forceinline__ bool kv4_word(const Kv4Span& s, int i, int64_t& tok, 
         rest = static_cast<int>(blockIdx.x - tok * s.parts) * s.span + static_cast<int>(li);
         return rest < s.row;
     }
-    const uint32_t t = s.row == 1 ? li : __umulhi(li, s.inv);
+    const uint32_t t = __umulhi(li, s.inv);
     rest = static_cast<int>(li - t * s.row);
     tok = static_cast<int64_t>(blockIdx.x) * s.tokens + t;
     return static_cast<int>(t) < s.tokens && tok < s.n;
 }
 
-// Thread = 8 channels of a token and head, ITEMS of them at a time; four neighbouring lanes hold a group and
-// find its largest magnitude by two shuffles.  One pass: each value is read once, codes leave as one 4-byte
-// word per lane.  16411 tokens of 8 heads of 128 (67 MB in, 19 MB out, 13.4 us at the copy rate) take 28.8 us:
-// the instructions of the quotients, codes and indexes (issue slots 75% busy) bound it, not the traffic; with
-// the codes replaced by a sum it takes 20.
+// Thread = W words of 8 channels of a token and head, ITEMS times; 4 / W neighbouring lanes hold a group and find
+// its largest magnitude by shuffles.  One pass: each value is read once, codes leave as one 4-byte
+// word per lane.  16411 tokens of 8 heads of 128 (67 MB in, 19 MB out, 13.4 us at the copy rate) take 26.8 us
+// with W = 2 (28.8 with one word a thread, issue slots 75% busy; 20 with the codes replaced by a sum).
 
-template <bool BF16, int ITEMS>
+template <bool BF16, int ITEMS, int W>
 __global__ void __launch_bounds__(kKvBlock)
 kv4_append_kernel(const Kv4View c, const Kv4Span s, const void* __restrict__ k, const void* __restrict__ v,
                   int64_t k_stride, int64_t v_stride, const int* __restrict__ slots) {
     pdl_launch_dependents();
     pdl_wait();
+    constexpr int kRaw = (BF16 ? 1 : 2) * W;                          // 16-byte loads per unit of W words
     const bool isv = blockIdx.y != 0;
-    const void* const src = isv ? v : k;
-    const int64_t stride = isv ? v_stride : k_stride;
-    const int lw = c.dim == 128 ? 4 : 3, sh = __ffs(c.page) - 1;      // log2 of words per head
-    uint4 raw[ITEMS][BF16 ? 1 : 2];
+    const char* const src = static_cast<const char*>(isv ? v : k);
+    const int64_t stride = (isv ? v_stride : k_stride) * (BF16 ? 2 : 4);
+    const int lu = (c.dim == 128 ? 4 : 3) - (W == 2 ? 1 : 0), sh = __ffs(c.page) - 1;      // log2 of units per head
+    uint4 raw[ITEMS][kRaw];
     int slot[ITEMS], at[ITEMS];
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
         int64_t tok;
         slot[i] = -1;
 #pragma unroll
-        for (int h = 0; h < (BF16 ? 1 : 2); ++h) raw[i][h] = make_uint4(0u, 0u, 0u, 0u);
+        for (int h = 0; h < kRaw; ++h) raw[i][h] = make_uint4(0u, 0u, 0u, 0u);
         if (kv4_word(s, i, tok, at[i])) {
             slot[i] = __ldg(slots + tok);
             if (slot[i] >= 0 && (slot[i] >> sh) < c.pages) {
-                const uint4* a = BF16 ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + tok * stride + at[i] * 8)
-                                      : reinterpret_cast<const uint4*>(static_cast<const float*>(src) + tok * stride + at[i] * 8);
+                const uint4* a = reinterpret_cast<const uint4*>(src + tok * stride) + at[i] * kRaw;
 #pragma unroll
-                for (int h = 0; h < (BF16 ? 1 : 2); ++h) raw[i][h] = __ldcs(a + h);
+                for (int h = 0; h < kRaw; ++h) raw[i][h] = __ldcs(a + h);
             } else {
                 slot[i] = -1;
             }
@@ -299,38 +300,51 @@ kv4_append_kernel(const Kv4View c, const Kv4Span s, const void* __restrict__ k, 
     }
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-        float x[8];
-        if (BF16) {
-            const uint32_t q[4] = {raw[i][0].x, raw[i][0].y, raw[i][0].z, raw[i][0].w};
+        float x[W][8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[2 * j] = __uint_as_float(q[j] << 16);
-                x[2 * j + 1] = __uint_as_float(q[j] & 0xFFFF0000u);
+        for (int w = 0; w < W; ++w) {
+            if (BF16) {
+                const uint32_t q[4] = {raw[i][w].x, raw[i][w].y, raw[i][w].z, raw[i][w].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[w][2 * j] = __uint_as_float(q[j] << 16);
+                    x[w][2 * j + 1] = __uint_as_float(q[j] & 0xFFFF0000u);
+                }
+            } else {
+                const uint4 a = raw[i][(2 * w) % kRaw], b = raw[i][(2 * w + 1) % kRaw];
+                x[w][0] = __uint_as_float(a.x); x[w][1] = __uint_as_float(a.y);
+                x[w][2] = __uint_as_float(a.z); x[w][3] = __uint_as_float(a.w);
+                x[w][4] = __uint_as_float(b.x); x[w][5] = __uint_as_float(b.y);
+                x[w][6] = __uint_as_float(b.z); x[w][7] = __uint_as_float(b.w);
             }
-        } else {
-            const uint4 a = raw[i][0], b = raw[i][BF16 ? 0 : 1];
-            x[0] = __uint_as_float(a.x); x[1] = __uint_as_float(a.y); x[2] = __uint_as_float(a.z); x[3] = __uint_as_float(a.w);
-            x[4] = __uint_as_float(b.x); x[5] = __uint_as_float(b.y); x[6] = __uint_as_float(b.z); x[7] = __uint_as_float(b.w);
         }
         float m = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[j]));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));       // a group's four words are in one token: row is a
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));       // multiple of 8
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[w][j]));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));             // the 4 / W lanes of a group are in one token:
+        if (W == 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2)); // a token has a multiple of 8 words
         if (slot[i] < 0) continue;
         float step;
-        uint32_t word;
+        uint32_t word[W];
         if (m <= 0x1p102f) {
-            word = kv4_pack8(x, m, step);
+            float r;
+            step = kv4_step_fast(m, r);
+#pragma unroll
+            for (int w = 0; w < W; ++w) word[w] = kv4_pack8(x[w], step, r);
         } else {
             step = kv4_step(m);
-            word = kv4_pack8_any(x, step);
+#pragma unroll
+            for (int w = 0; w < W; ++w) word[w] = kv4_pack8_any(x[w], step);
         }
-        const int head = at[i] >> lw, w = at[i] & ((1 << lw) - 1);
+        const int head = at[i] >> lu, u = at[i] & ((1 << lu) - 1);
         const int64_t cell = (static_cast<int64_t>(slot[i] >> sh) * c.heads + head) * c.page + (slot[i] & (c.page - 1));
-        reinterpret_cast<uint32_t*>(isv ? c.vc : c.kc)[(cell << lw) + w] = word;
-        if ((w & 3) == 0)
-            (isv ? c.vs : c.ks)[(cell << (lw - 2)) + (w >> 2)] = static_cast<uint16_t>(__float_as_uint(step) >> 16);
+        uint32_t* to = reinterpret_cast<uint32_t*>(isv ? c.vc : c.kc) + ((cell << lu) + u) * W;
+        if (W == 2) *reinterpret_cast<uint2*>(to) = make_uint2(word[0], word[W - 1]);
+        else *to = word[0];
+        if ((u & (4 / W - 1)) == 0)
+            (isv ? c.vs : c.ks)[(cell << (lu - (W == 2 ? 1 : 2))) + u / (4 / W)] = static_cast<uint16_t>(__float_as_uint(step) >> 16);
     }
 }
 

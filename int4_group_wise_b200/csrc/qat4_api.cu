@@ -864,7 +864,7 @@ static qat4::Kv4View kv4_view(const qat4_kv4_cache* c) {
     return {c->k_codes, c->k_scales, c->v_codes, c->v_scales, c->num_pages, c->page_size, c->kv_heads, c->head_dim};
 }
 
-// Blocks over the 8-channel words of n tokens of k and v: `row` words a token, a multiple of 8 and at most 16384.
+// Blocks over the units (8 or 16 channels) of n tokens of k and v: `row` units a token, at least 4 and at most 16384.
 // `items` words per thread: several in flight once the batch has blocks enough for every SM (48 tokens of 8
 // heads of 128: 1.9 us with one, 3.1 with four; 16411 tokens: 40 and 30).
 static int kv4_items(int64_t n, int64_t row) { return n * row >= 4 * 148 * qat4::kKvBlock ? qat4::kKvItems : 1; }
@@ -901,12 +901,12 @@ static bool launch_pdl(void (*kernel)(P...), dim3 grid, int block, size_t smem, 
     return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
-template <bool BF16, int ITEMS>
+template <bool BF16, int ITEMS, int W>
 static bool kv4_append_launch(const qat4_kv4_cache* cache, const void* k, const void* v, int64_t k_stride,
                               int64_t v_stride, const int32_t* slots, int64_t n, int64_t row, cudaStream_t stream) {
     dim3 grid;
-    const qat4::Kv4Span s = kv4_span(n, row, ITEMS, &grid);
-    return launch_pdl(qat4::kv4_append_kernel<BF16, ITEMS>, grid, qat4::kKvBlock, 0, stream, 1, kv4_view(cache), s, k, v,
+    const qat4::Kv4Span s = kv4_span(n, row / W, ITEMS, &grid);
+    return launch_pdl(qat4::kv4_append_kernel<BF16, ITEMS, W>, grid, qat4::kKvBlock, 0, stream, 1, kv4_view(cache), s, k, v,
                       k_stride, v_stride, slots);
 }
 
@@ -1018,10 +1018,10 @@ qat4_status qat4_kv4_append(const qat4_kv4_cache* cache, const void* k, const vo
     if (n == 0) return QAT4_OK;
     const bool many = kv4_items(n, row / 8) > 1;
     const bool ok = dtype == QAT4_BF16
-        ? (many ? kv4_append_launch<true, qat4::kKvItems>(cache, k, v, k_stride, v_stride, slots, n, row / 8, stream)
-                : kv4_append_launch<true, 1>(cache, k, v, k_stride, v_stride, slots, n, row / 8, stream))
-        : (many ? kv4_append_launch<false, qat4::kKvItems>(cache, k, v, k_stride, v_stride, slots, n, row / 8, stream)
-                : kv4_append_launch<false, 1>(cache, k, v, k_stride, v_stride, slots, n, row / 8, stream));
+        ? (many ? kv4_append_launch<true, 2, 2>(cache, k, v, k_stride, v_stride, slots, n, row / 8, stream)
+                : kv4_append_launch<true, 1, 1>(cache, k, v, k_stride, v_stride, slots, n, row / 8, stream))
+        : (many ? kv4_append_launch<false, 2, 2>(cache, k, v, k_stride, v_stride, slots, n, row / 8, stream)
+                : kv4_append_launch<false, 1, 1>(cache, k, v, k_stride, v_stride, slots, n, row / 8, stream));
     return ok ? QAT4_OK : QAT4_ERR_CUDA;
 }
 
