@@ -87,11 +87,11 @@ struct Request {
 };
 __device__ __forceinline__ Request kv4_request(const AttnParams& p, int b) {
     Request r;
-    const int a = min(max(__ldg(p.cu_q + b), 0), p.N), e = min(max(__ldg(p.cu_q + b + 1), 0), p.N);
+    const int a = min(max(kv4_ld(p.cu_q + b), 0), p.N), e = min(max(kv4_ld(p.cu_q + b + 1), 0), p.N);
     r.q0 = a;
     r.nq = max(0, e - a);
     const int64_t cap = static_cast<int64_t>(p.max_blocks) * p.c.page;
-    const int len = max(0, __ldg(p.seq_lens + b));
+    const int len = max(0, kv4_ld(p.seq_lens + b));
     r.len = static_cast<int>(len < cap ? len : cap);
     r.first = r.len - r.nq;
     r.lo = p.window > 0 ? max(0, r.first - p.window + 1) : 0;
@@ -344,7 +344,7 @@ kv4_decode_kernel(const AttnParams p) {
         auto entry = [&](const Place<ROWS>& x) -> int {
             const int pt = x.t0() + pi * page;                 // first token of this lane's page
             // pt < len keeps the index inside the table's row
-            return has && pt < x.r.len && pt + page > x.r.lo ? __ldg(p.table + x.b * p.table_stride + (pt >> sh)) : -1;
+            return has && pt < x.r.len && pt + page > x.r.lo ? kv4_ld(p.table + x.b * p.table_stride + (pt >> sh)) : -1;
         };
         int64_t issued = 0;
         int s = 0;
@@ -436,7 +436,7 @@ kv4_decode_kernel(const AttnParams p) {
                     for (int w = 0; w < kW; ++w) {
                         if (kQs && (n * kW + w) % kKaWarps != warp) continue;        // the warps share this work
                         uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                        if (in) x = __ldg(reinterpret_cast<const uint4*>(src) + w);
+                        if (in) x = kv4_ld(reinterpret_cast<const uint4*>(src) + w);
                         const uint32_t y[4] = {__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
                                                __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632)};
 #pragma unroll

@@ -19,6 +19,12 @@
 
 namespace qat4 {
 
+// A plain load.  These kernels may become resident before the kernel that writes what they read has run, so
+// nothing of that goes through the read-only path, which supposes data that no one writes while the
+// kernel lives: no read-only intrinsic, no restrict-qualified input.
+template <typename T>
+__device__ __forceinline__ T kv4_ld(const T* p) { return *p; }
+
 // mbar_wait with its loop out of line: the kernels below wait in many places, and their code is kept small.
 __device__ __noinline__ bool kv4_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
     return mbar_wait(bar, parity, abort, limit_ns);
@@ -270,8 +276,8 @@ __device__ __forceinline__ bool kv4_word(const Kv4Span& s, int i, int64_t& tok, 
 
 template <bool BF16, int ITEMS, int W>
 __global__ void __launch_bounds__(kKvBlock)
-kv4_append_kernel(const Kv4View c, const Kv4Span s, const void* __restrict__ k, const void* __restrict__ v,
-                  int64_t k_stride, int64_t v_stride, const int* __restrict__ slots) {
+kv4_append_kernel(const Kv4View c, const Kv4Span s, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                  const int* slots) {
     pdl_launch_dependents();
     pdl_wait();
     constexpr int kRaw = (BF16 ? 1 : 2) * W;                          // 16-byte loads per unit of W words
@@ -288,7 +294,7 @@ kv4_append_kernel(const Kv4View c, const Kv4Span s, const void* __restrict__ k, 
 #pragma unroll
         for (int h = 0; h < kRaw; ++h) raw[i][h] = make_uint4(0u, 0u, 0u, 0u);
         if (kv4_word(s, i, tok, at[i])) {
-            slot[i] = __ldg(slots + tok);
+            slot[i] = kv4_ld(slots + tok);
             if (slot[i] >= 0 && (slot[i] >> sh) < c.pages) {
                 const uint4* a = reinterpret_cast<const uint4*>(src + tok * stride) + at[i] * kRaw;
 #pragma unroll
@@ -370,8 +376,7 @@ __device__ __forceinline__ uint32_t kv4_off(uint32_t step2) {
 // copy rate, 16.3 measured).
 template <int ITEMS>
 __global__ void __launch_bounds__(kKvBlock)
-kv4_gather_kernel(const Kv4View c, const Kv4Span s, const int* __restrict__ slots, uint16_t* __restrict__ k,
-                  uint16_t* __restrict__ v) {
+kv4_gather_kernel(const Kv4View c, const Kv4Span s, const int* slots, uint16_t* k, uint16_t* v) {
     pdl_launch_dependents();
     pdl_wait();
     const bool isv = blockIdx.y != 0;
@@ -388,7 +393,7 @@ kv4_gather_kernel(const Kv4View c, const Kv4Span s, const int* __restrict__ slot
         q[i] = st[i] = 0;
         if (!kv4_word(s, i, tok, rest)) continue;
         to[i] = tok * s.row + rest;
-        const int slot = __ldg(slots + tok);
+        const int slot = kv4_ld(slots + tok);
         if (slot < 0 || (slot >> sh) >= c.pages) continue;
         const int head = rest >> lw, w = rest & ((1 << lw) - 1);
         const int64_t cell = (static_cast<int64_t>(slot >> sh) * c.heads + head) * c.page + (slot & (c.page - 1));

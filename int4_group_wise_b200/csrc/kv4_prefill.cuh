@@ -147,10 +147,10 @@ __device__ __forceinline__ void kp_load(KpRow<D>& r, const uint8_t* codes, const
     if (in) {
         const uint4* c = reinterpret_cast<const uint4*>(codes + cell * (D / 2));
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) r.w[i] = __ldg(c + i);
+        for (int i = 0; i < D / 32; ++i) r.w[i] = kv4_ld(c + i);
         const uint32_t* s = reinterpret_cast<const uint32_t*>(steps + cell * (D / 32));
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) r.st[i] = __ldg(s + i);
+        for (int i = 0; i < D / 64; ++i) r.st[i] = kv4_ld(s + i);
     }
 }
 // The row as operand row `row` (128-byte swizzle, 64 channels per 16 KB half).
@@ -177,11 +177,8 @@ struct KpItem {
     int t_first, n, split;    // first key, blocks of 128 keys
 };
 
-// Item `idx` of the grid, found by a converged warp: split, kv head, and the rank of its row tile, the
-// last (longest) tile of a request first.  Up to 32 requests are taken from the longest to the
-// shortest, so that short items even out the end; more are taken 32 by 32 as they come, and `first`
-// holds the tiles before each 32 of them (`groups` entries and the total).  False where there are fewer tiles.
 constexpr int kKpGroups = 2048;                    // 32 requests each
+// Row tiles before each 32 requests, and all of them (`groups` + 1 entries), by a converged warp.
 __device__ __noinline__ void kp_groups(const PrefillParams& pp, int* first, int groups, int lane) {
     int sum = 0;
     for (int g = 0; g < groups; ++g) {
@@ -192,6 +189,10 @@ __device__ __noinline__ void kp_groups(const PrefillParams& pp, int* first, int 
     if (lane == 0) first[groups] = sum;
     __syncwarp();
 }
+// Item `idx` of the grid, found by a converged warp: split, kv head, and the rank of its row tile, the
+// last (longest) tile of a request first.  Requests are taken 32 by 32 (`first` has the tiles before each
+// 32, when there are more), and of these from the longest to the shortest, so that short items even out the
+// end.  False where there are fewer tiles.
 __device__ __forceinline__ bool kp_locate(const PrefillParams& pp, const int* first, int groups, int idx, int lane, KpItem& it) {
     const AttnParams& p = pp.a;
     it.split = idx % pp.splits;
@@ -338,7 +339,7 @@ kv4_prefill_kernel(const PrefillParams pp) {
 #pragma unroll
                 for (int w = 0; w < D / 8; ++w) {
                     v[w] = make_uint4(0u, 0u, 0u, 0u);
-                    if (in) v[w] = __ldg(src + w);
+                    if (in) v[w] = kv4_ld(src + w);
                 }
 #pragma unroll
                 for (int w = 0; w < D / 8; ++w)
@@ -414,7 +415,7 @@ kv4_prefill_kernel(const PrefillParams pp) {
             auto entry = [&](int t0) -> int {
                 const int t = t0 + lane * page;
                 if (lane >= (kKpBlock >> sh) || t >= it.len) return 0;
-                const int id = __ldg(trow + (t >> sh));
+                const int id = kv4_ld(trow + (t >> sh));
                 return id < 0 || id >= p.c.pages ? -1 : 0;
             };
             int id = entry(it.t_first);
@@ -511,7 +512,7 @@ kv4_prefill_kernel(const PrefillParams pp) {
                 live = j < it.n && t < it.len && t >= it.lo;
                 int id = 0;
                 if (live) {
-                    id = __ldg(p.table + it.b * p.table_stride + (t >> sh));
+                    id = kv4_ld(p.table + it.b * p.table_stride + (t >> sh));
                     live = id >= 0 && id < p.c.pages;
                 }
                 return (static_cast<int64_t>(id) * p.c.heads + it.kvh) * page + (t & (page - 1));
