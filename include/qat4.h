@@ -464,9 +464,11 @@ qat4_status qat4_kv4_gather(const qat4_kv4_cache *cache, const int32_t *slots, i
  *  window    0: no limit; w > 0 (causal only): the last w positions, its own
  *            included.
  *  out       bf16 bit patterns [N, q_heads, head_dim].  A query that sees no key
- *            gives zeros.
+ *            gives zeros.  It may be q itself (q_stride = q_heads * head_dim), and
+ *            overlaps no input otherwise.
  *  lse       float32 [N, q_heads] (may be NULL): log of the sum of exp(scale q.k),
- *            -infinity where no key is seen.
+ *            -infinity where no key is seen, NaN (as the row of out) for a NaN
+ *            in q.
  *  workspace device scratch of at least qat4_kv4_attention_workspace_bytes bytes
  *            (may be NULL when that is 0), 16-byte aligned; contents on entry are ignored.  Calls that may
  *            overlap on the GPU (other streams, two captured graphs) need one

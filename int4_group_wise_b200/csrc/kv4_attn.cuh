@@ -195,6 +195,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     return v;
 }
 
+// log-sum-exp of a row from its reference maximum (log2) and sum: -infinity where no key was seen, NaN where a
+// score was.
+__device__ __forceinline__ float kv4_lse(float m, float l) {
+    return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
 // Row `row` of a tile's result: out (and lse) from the unnormalised sums.
 __device__ __forceinline__ int64_t ka_out_row(const AttnParams& p, const Request& r, int kvh, int row) {
     const int tok = row / p.group;
@@ -704,7 +710,7 @@ kv4_decode_kernel(const AttnParams p) {
                         *reinterpret_cast<uint4*>(p.out + to * D + d0) =
                             make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
                                        pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv));
-                        if (d0 == 0 && p.lse) p.lse[to] = ll > 0.0f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+                        if (d0 == 0 && p.lse) p.lse[to] = kv4_lse(mm, ll);
                     } else {
                         float4* dst = reinterpret_cast<float4*>(piece + row * D + d0);
                         dst[0] = make_float4(o[0], o[1], o[2], o[3]);
@@ -765,7 +771,7 @@ kv4_decode_kernel(const AttnParams p) {
             const int64_t to = ka_out_row(p, r, kvh, tile * ROWS + row);
             *reinterpret_cast<uint2*>(p.out + to * D + d0) =
                 make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-            if (d0 == 0 && p.lse) p.lse[to] = ll > 0.0f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+            if (d0 == 0 && p.lse) p.lse[to] = kv4_lse(mm, ll);
         }
         __syncwarp();
         cluster_sync_all();      // no CTA leaves while another may still read its piece
@@ -863,7 +869,7 @@ kv4_combine_kernel(const AttnParams p, int ctas) {
     for (int k = 0; k < kC; k += 2)
         dst[k / 2] = pack_bf16((o[k] * f0 + part[q][kC * lane + k] * f1) * inv,
                                (o[k + 1] * f0 + part[q][kC * lane + k + 1] * f1) * inv);
-    if (lane == 0 && p.lse) p.lse[at] = ll > 0.0f ? (top + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+    if (lane == 0 && p.lse) p.lse[at] = kv4_lse(top, ll);
 }
 
 }  // namespace qat4

@@ -389,7 +389,7 @@ kv4_prefill_kernel(const PrefillParams pp) {
                 }
                 if (held_in) {
                     if (whole) {
-                        if (p.lse) p.lse[held_at] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                        if (p.lse) p.lse[held_at] = kv4_lse(m, l);
                     } else {
                         float* st = pp.part + pp.splits * all * D;
                         st[held_split * all + held_at] = m;
@@ -732,7 +732,7 @@ kv4_join_kernel(const PrefillParams pp) {
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * D + lane * (D / 32));
 #pragma unroll
     for (int i = 0; i < D / 32; i += 2) dst[i / 2] = pack_bf16(o[i] * inv, o[i + 1] * inv);
-    if (lane == 0 && p.lse) p.lse[at] = ll > 0.0f ? (mm + log2f(ll)) * 0.6931471805599453f : -INFINITY;
+    if (lane == 0 && p.lse) p.lse[at] = kv4_lse(mm, ll);
 }
 
 }  // namespace qat4

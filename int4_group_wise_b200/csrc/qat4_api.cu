@@ -898,7 +898,9 @@ static bool launch_pdl(void (*kernel)(P...), dim3 grid, int block, size_t smem, 
     cfg.stream = stream;
     cfg.attrs = pdl;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return true;
+    cudaGetLastError();      // reported by this call, not by the next one
+    return false;
 }
 
 template <bool BF16, int ITEMS, int W>

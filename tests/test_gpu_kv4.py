@@ -333,6 +333,28 @@ def test_attention_window_of_any_size():
             assert torch.equal(got[0].view(torch.int16), want[0].view(torch.int16)) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("lens,nqs,q_heads", [
+    ([300, 40], [1, 1], 4), ([5000, 300], [1, 1], 4), ([300, 40], [2, 2], 4), ([300, 40], [4, 4], 4), ([5000], [4], 4),
+    ([150] * 70, [5] * 70, 4), ([300], [300], 4), ([5000], [40], 4), ([600, 300], [130, 1], 4)])
+def test_attention_nan_queries_stay_in_their_rows(lens, nqs, q_heads):
+    """A NaN in one query head gives NaN there, in the output and in the log-sum-exp, and leaves every other row's
+    bits alone; the output may take the queries' place."""
+    for dim in (64, 128):
+        q, cache, table, lens_t, cu = _batch(lens, nqs, 64, 1, dim, q_heads, seed=dim)
+        out, lse = _run(q, cache, table, lens_t, cu)
+        at = int(cu[-1]) // 2
+        dirty = q.clone()
+        dirty[at, 1, 5] = math.nan
+        got, gl = _run(dirty, cache, table, lens_t, cu)
+        assert bool(torch.isnan(got[at, 1]).all()) and math.isnan(float(gl[at, 1]))
+        got[at, 1], gl[at, 1] = out[at, 1], lse[at, 1]
+        assert torch.equal(got.view(torch.int16), out.view(torch.int16)) and torch.equal(gl, lse)
+        place = q.cuda()
+        q4.kv4_attention(place, q4.KV4Cache(*(t.cuda() for t in cache)), table.cuda(), lens_t.cuda(), cu.cuda(), out=place)
+        q4.sync_check()
+        assert torch.equal(place.cpu().view(torch.int16), out.view(torch.int16))
+
+
 def test_attention_large_and_small_scores():
     """Scores that leave one key all the weight, equal scores, and a scale other than 1/sqrt(D)."""
     q, cache, table, lens, cu = _batch([300, 129, 700], [1, 20, 300], 64, 1, 128, 4, seed=6)
