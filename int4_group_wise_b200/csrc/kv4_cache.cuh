@@ -204,24 +204,29 @@ __device__ __forceinline__ float kv4_step(float m) {
     return d < 0x1p-100f ? 0.0f : fminf(up, 0x1p100f);
 }
 
-// Eight values as packed codes, two's-complement nibbles, value i at bits 4i.  Any step and any values.
-__device__ __noinline__ uint32_t kv4_pack8_any(const float (&v)[8], float step) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float q = code_of(scaled_exact(v[i], step));
-        w |= (static_cast<uint32_t>(static_cast<int>(q)) & 15u) << (4 * i);
-    }
-    return w;
+// Eight values as packed codes, two's-complement nibbles, value i at bits 4i.  Any step and any values, which come
+// in registers (an array by reference would be kept in local memory by the callers' common path too).
+__device__ __forceinline__ uint32_t kv4_nibble(float v, float step) {
+    return static_cast<uint32_t>(static_cast<int>(code_of(scaled_exact(v, step)))) & 15u;
 }
-// The same for groups whose largest magnitude m is at most 2^102, with the step.  Both quotients, fl(m / 7)
-// and fl(v / step), come from an approximate reciprocal r (within 1 ulp) by Markstein's correction
-// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990):
-// q0 = fl(v r), e = v - q0 d exactly by one FMA, q = fl(q0 + e r).  A quotient of a 24-bit significand by one
-// of at most 5 bits is at least 2^-31 of itself from the nearest rounding boundary, and q0 + e r within 2^-44,
-// so q is the IEEE quotient (below 2^-100, where e may lose bits, the step is 0 and every code too).  Cutting
-// q to [-8, 7] before it is rounded changes no code; adding 1.5 * 2^23 rounds it half to even and leaves the
-// code in the low bits.
+__device__ __noinline__ uint32_t kv4_pack8_any(float4 a, float4 b, float step) {
+    return kv4_nibble(a.x, step) | kv4_nibble(a.y, step) << 4 | kv4_nibble(a.z, step) << 8 | kv4_nibble(a.w, step) << 12 |
+           kv4_nibble(b.x, step) << 16 | kv4_nibble(b.y, step) << 20 | kv4_nibble(b.z, step) << 24 | kv4_nibble(b.w, step) << 28;
+}
+// The same for groups without a NaN and with largest magnitude m at most 2^102, with the step.  There
+// |v / step| < 7.001, so nothing is cut, and each code leaves as code + 8 in the low bits of
+// 1.5 * 2^23 + 8 + code; multiplying the sum so far by 16 packs it in one integer FMA, and one subtraction
+// and one exclusive or at the end take off what the words' upper bits and the eights have added.
+// The quotients come from an approximate reciprocal r of the step (within 1 ulp):
+// fl(m / 7), and float32 values, by Markstein's correction (P. Markstein, "Computation of elementary functions
+//   on the IBM RISC System/6000 processor", 1990): q0 = fl(v r), e = v - q0 d exactly by one FMA, q = fl(q0 + e r).
+//   A quotient of a 24-bit significand by one of at most 5 bits is at least 2^-31 of itself from the nearest
+//   rounding boundary, and q0 + e r within 2^-44, so q is the IEEE quotient (below 2^-100, where e may lose bits,
+//   the step is 0 and every code too).
+// bf16 values need only which code is nearest.  v = V 2^a and step = S 2^b with V < 2^8, S < 2^5, so 2 v and
+//   (2 k + 1) step, if they differ, differ by 2^(a + 1) or 2^b at least: v / step is k + 1/2 or farther than
+//   2^-10 from it.  One FMA rounds v r to a multiple of 2^-11 (with 1.5 * 2^12 in front): exact halves become
+//   exact halves again, the others stay on their side, and the addition of 1.5 * 2^23 rounds half to even.
 __device__ __forceinline__ float kv4_quotient(float a, float d, float r) {
     const float q0 = __fmul_rn(a, r);
     return __fmaf_rn(__fmaf_rn(-q0, d, a), r, q0);
@@ -231,17 +236,31 @@ __device__ __forceinline__ float kv4_step_fast(float m, float& r) {
     const float up = __uint_as_float((__float_as_uint(d) + 0x7FFFFu) & ~0x7FFFFu);
     const float step = d < 0x1p-100f ? 0.0f : fminf(up, 0x1p100f);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(step));
+    if (step == 0.0f) r = 0.0f;                                       // then every quotient is 0
     return step;
 }
+template <bool BF16>
 __device__ __forceinline__ uint32_t kv4_pack8(const float (&v)[8], float step, float r) {
+    constexpr float kEight = 0x1.8p23f + 8.0f;
     uint32_t w = 0;
 #pragma unroll
     for (int i = 7; i >= 0; --i) {
-        const float q = kv4_quotient(v[i], step, r);
-        const uint32_t c = __float_as_uint(__fadd_rn(fminf(fmaxf(q, kQmin), kQmax), 12582912.0f));
-        w = (w << 4) | (c & 15u);
+        const float u = BF16 ? __fadd_rn(__fmaf_rn(v[i], r, 0x1.8p12f), kEight - 0x1.8p12f)
+                             : __fadd_rn(kv4_quotient(v[i], step, r), kEight);
+        w = w * 16u + __float_as_uint(u);
     }
-    return step == 0.0f ? 0u : w;
+    return (w - 0x4B400000u * 0x11111111u) ^ 0x88888888u;
+}
+// The larger one, NaN if either is.
+__device__ __forceinline__ float kv4_max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t kv4_max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
 
 constexpr int kKvBlock = 256;
@@ -270,10 +289,10 @@ __device__ __forceinline__ bool kv4_word(const Kv4Span& s, int i, int64_t& tok, 
 }
 
 // Thread = W words of 8 channels of a token and head, ITEMS times; 4 / W neighbouring lanes hold a group and find
-// its largest magnitude by shuffles.  One pass: each value is read once, codes leave as one 4-byte
-// word per lane.  16411 tokens of 8 heads of 128 (67 MB in, 19 MB out, 13.4 us at the copy rate) take 26.8 us
-// with W = 2 (28.8 with one word a thread, issue slots 75% busy; 20 with the codes replaced by a sum).
-
+// its largest magnitude by shuffles.  One pass: each value is read once, a thread's codes leave in one store.
+// Bound: HBM.  16411 tokens of 8 heads of 128 (67 MB in, 19 MB out, 13.4 us at the copy rate) take 17.2 us with two
+// times two words a thread (18.4 with one time two, 25.6 with one word: half the bytes in flight per thread, and
+// twice the work on steps).
 template <bool BF16, int ITEMS, int W>
 __global__ void __launch_bounds__(kKvBlock)
 kv4_append_kernel(const Kv4View c, const Kv4Span s, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
@@ -294,14 +313,12 @@ kv4_append_kernel(const Kv4View c, const Kv4Span s, const void* k, const void* v
 #pragma unroll
         for (int h = 0; h < kRaw; ++h) raw[i][h] = make_uint4(0u, 0u, 0u, 0u);
         if (kv4_word(s, i, tok, at[i])) {
-            slot[i] = kv4_ld(slots + tok);
-            if (slot[i] >= 0 && (slot[i] >> sh) < c.pages) {
-                const uint4* a = reinterpret_cast<const uint4*>(src + tok * stride) + at[i] * kRaw;
+            // the values do not wait for the slot (rows without one are read for nothing)
+            const uint4* a = reinterpret_cast<const uint4*>(src + tok * stride) + at[i] * kRaw;
 #pragma unroll
-                for (int h = 0; h < kRaw; ++h) raw[i][h] = __ldcs(a + h);
-            } else {
-                slot[i] = -1;
-            }
+            for (int h = 0; h < kRaw; ++h) raw[i][h] = __ldcs(a + h);
+            slot[i] = kv4_ld(slots + tok);
+            if ((slot[i] >> sh) >= c.pages) slot[i] = -1;
         }
     }
 #pragma unroll
@@ -324,13 +341,24 @@ kv4_append_kernel(const Kv4View c, const Kv4Span s, const void* k, const void* v
                 x[w][6] = __uint_as_float(b.z); x[w][7] = __uint_as_float(b.w);
             }
         }
+        // the group's largest magnitude, NaN if it holds one (bf16: magnitudes as integers, in pairs)
         float m = 0.0f;
+        if (BF16) {
+            uint32_t y = 0u;
 #pragma unroll
-        for (int w = 0; w < W; ++w)
+            for (int w = 0; w < W; ++w) {
+                y = kv4_max_u16x2(y, kv4_max_u16x2(raw[i][w].x & 0x7FFF7FFFu, raw[i][w].y & 0x7FFF7FFFu));
+                y = kv4_max_u16x2(y, kv4_max_u16x2(raw[i][w].z & 0x7FFF7FFFu, raw[i][w].w & 0x7FFF7FFFu));
+            }
+            m = kv4_max_nan(__uint_as_float(y << 16), __uint_as_float(y & 0xFFFF0000u));
+        } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[w][j]));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));             // the 4 / W lanes of a group are in one token:
-        if (W == 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2)); // a token has a multiple of 8 words
+            for (int w = 0; w < W; ++w)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m = kv4_max_nan(m, fabsf(x[w][j]));
+        }
+        m = kv4_max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));              // the 4 / W lanes of a group are in one
+        if (W == 1) m = kv4_max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));  // token: it has a multiple of 8 words
         if (slot[i] < 0) continue;
         float step;
         uint32_t word[W];
@@ -338,11 +366,23 @@ kv4_append_kernel(const Kv4View c, const Kv4Span s, const void* k, const void* v
             float r;
             step = kv4_step_fast(m, r);
 #pragma unroll
-            for (int w = 0; w < W; ++w) word[w] = kv4_pack8(x[w], step, r);
+            for (int w = 0; w < W; ++w) word[w] = kv4_pack8<BF16>(x[w], step, r);
         } else {
+            // very large values, or a NaN, which does not count for the step; the group's lanes are all here
+            constexpr int kLanes = 4 / W;
+            const uint32_t lanes = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(kLanes - 1));
+            m = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(x[w][j]));
+#pragma unroll
+            for (int d = 1; d < kLanes; d <<= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, d));
             step = kv4_step(m);
 #pragma unroll
-            for (int w = 0; w < W; ++w) word[w] = kv4_pack8_any(x[w], step);
+            for (int w = 0; w < W; ++w)
+                word[w] = kv4_pack8_any(make_float4(x[w][0], x[w][1], x[w][2], x[w][3]),
+                                        make_float4(x[w][4], x[w][5], x[w][6], x[w][7]), step);
         }
         const int head = at[i] >> lu, u = at[i] & ((1 << lu) - 1);
         const int64_t cell = (static_cast<int64_t>(slot[i] >> sh) * c.heads + head) * c.page + (slot[i] & (c.page - 1));

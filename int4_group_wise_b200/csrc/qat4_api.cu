@@ -864,10 +864,13 @@ static qat4::Kv4View kv4_view(const qat4_kv4_cache* c) {
     return {c->k_codes, c->k_scales, c->v_codes, c->v_scales, c->num_pages, c->page_size, c->kv_heads, c->head_dim};
 }
 
-// Blocks over the units (8 or 16 channels) of n tokens of k and v: `row` units a token, at least 4 and at most 16384.
-// `items` words per thread: several in flight once the batch has blocks enough for every SM (48 tokens of 8
-// heads of 128: 1.9 us with one, 3.1 with four; 16411 tokens: 40 and 30).
-static int kv4_items(int64_t n, int64_t row) { return n * row >= 4 * 148 * qat4::kKvBlock ? qat4::kKvItems : 1; }
+// Blocks over the units (8 or 16 channels) of n tokens of k and v: `row` units a token, at least 4 and at most 16384;
+// `items` units per thread.
+// Large batches, of `least` words and more for every thread of a block on each SM, take several words per thread.
+// Tokens of 8 heads of 128, one word a thread and several, us: append bf16 1184: 2.7, 3.8; 2400: 5.1, 4.4; 16411:
+// 25.6, 17.2.  append float32 2400: 5.5, 6.0; 4800: 9.3, 9.6; 16411: 27.5, 24.8.  gather 2400: 3.8, 5.0; 4800: 6.7,
+// 5.6; 16411: 19.1, 15.4.
+static bool kv4_many(int64_t n, int64_t row, int64_t least) { return n * row >= least * 148 * qat4::kKvBlock; }
 static qat4::Kv4Span kv4_span(int64_t n, int64_t row, int items, dim3* grid) {
     qat4::Kv4Span s;
     s.n = n;
@@ -1018,7 +1021,7 @@ qat4_status qat4_kv4_append(const qat4_kv4_cache* cache, const void* k, const vo
     if (k_stride % unit != 0 || v_stride % unit != 0 || !aligned16(k) || !aligned16(v) || !aligned4(slots))
         return QAT4_ERR_ALIGN;
     if (n == 0) return QAT4_OK;
-    const bool many = kv4_items(n, row / 8) > 1;
+    const bool many = kv4_many(n, row / 8, dtype == QAT4_BF16 ? 8 : 12);
     const bool ok = dtype == QAT4_BF16
         ? (many ? kv4_append_launch<true, 2, 2>(cache, k, v, k_stride, v_stride, slots, n, row / 8, stream)
                 : kv4_append_launch<true, 1, 1>(cache, k, v, k_stride, v_stride, slots, n, row / 8, stream))
@@ -1036,7 +1039,7 @@ qat4_status qat4_kv4_gather(const qat4_kv4_cache* cache, const int32_t* slots, i
     if (n < 0 || n >= (int64_t(1) << 31) || n * (row / 8) > (int64_t(1) << 40)) return QAT4_ERR_SHAPE;
     if (!aligned16(k) || !aligned16(v) || !aligned4(slots)) return QAT4_ERR_ALIGN;
     if (n == 0) return QAT4_OK;
-    const bool ok = kv4_items(n, row / 8) > 1 ? kv4_gather_launch<qat4::kKvItems>(cache, slots, n, row / 8, k, v, stream)
+    const bool ok = kv4_many(n, row / 8, 12) ? kv4_gather_launch<qat4::kKvItems>(cache, slots, n, row / 8, k, v, stream)
                                               : kv4_gather_launch<1>(cache, slots, n, row / 8, k, v, stream);
     return ok ? QAT4_OK : QAT4_ERR_CUDA;
 }

@@ -157,6 +157,40 @@ def test_append_and_gather(n, h, d, page, dtype, kind):
         assert torch.equal(got.cpu().double(), want)
 
 
+@pytest.mark.parametrize("n,h,d,page,dtype,kind", [
+    (4001, 8, 128, 64, torch.float32, "normal"), (4001, 8, 128, 16, torch.float32, "edges"),
+    (9001, 7, 64, 32, torch.bfloat16, "edges"), (5003, 6, 128, 128, torch.bfloat16, "grid")])
+def test_append_and_gather_large(n, h, d, page, dtype, kind):
+    """Batches large enough for several words per thread."""
+    test_append_and_gather(n, h, d, page, dtype, kind)
+
+
+@pytest.mark.parametrize("copies", [1, 9])
+def test_append_every_bf16_against_every_step(copies):
+    """All bf16 significands at every exponent that gives a code other than 0, and some below, against every 5-bit
+    step; some groups hold a NaN, an infinity or values near the type's ends.  Small and large batches."""
+    groups = []
+    for s in range(16, 32):
+        v = (torch.arange(256).float() * 2.0 ** -4)[None] * 2.0 ** torch.arange(-14, 8)[:, None].float()
+        v = v[v <= 7 * s / 16]
+        v = torch.cat([v, -v, torch.zeros(-2 * v.numel() % 31)]).view(-1, 31)
+        groups.append(torch.cat([torch.full((v.shape[0], 1), 7 * s / 16), v], 1))
+    x = torch.cat(groups)
+    x = torch.cat([x, x * 2.0 ** 90, x * 2.0 ** -90])
+    for i, bad in enumerate((math.nan, math.inf, -math.inf, 3e38, -1e-38)):
+        x[11 + 40 * i:3000:200, 7 * i] = bad
+    x[4000, :] = math.nan
+    x = x[: x.shape[0] // 4 * 4].view(-1, 1, 128).bfloat16()
+    q, s = ref.quantize(x)
+    n = x.shape[0]
+    cache = q4.kv4_cache(-(-copies * n // 16), 16, 1, 128)
+    q4.kv4_append(cache, x.repeat(copies, 1, 1).cuda(), x.flip(0).repeat(copies, 1, 1).cuda(),
+                  torch.arange(copies * n, dtype=I32).cuda())
+    flat = lambda t: t.cpu().transpose(1, 2).flatten(0, 1)[:copies * n].view(copies, n, 1, -1)  # noqa: E731
+    for codes, scales, wq, ws in ((cache.k_codes, cache.k_scales, q, s), (cache.v_codes, cache.v_scales, q.flip(0), s.flip(0))):
+        assert bool((flat(codes) == ref.pack(wq)).all()) and bool((flat(scales).float() == ws).all())
+
+
 def test_append_quantizer_error():
     """Against the values themselves: a code's value is off by at most half a step, and the step is at most
     17/16 of m / 7 (5 significant bits rounded up: at most one part in 16)."""
