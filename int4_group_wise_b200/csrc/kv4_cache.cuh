@@ -56,7 +56,8 @@ struct Kv4View {
 // takes its share of the table rows and of the tokens.  A new token's page is
 // computed from the free list, not read from the table, so no CTA waits for
 // another's writes.  Bound by launch latency up to some ten thousand tokens,
-// then by the 4 bytes written per token.
+// then by the 4 bytes written per token: replayed from a graph, 32 requests with
+// one token each take 5.7 us, 1000 requests with 511,000 tokens 8.2.
 constexpr int kTbThreads = 512;
 constexpr int kTbMaxRequests = 16384;
 
