@@ -264,28 +264,36 @@ __device__ __forceinline__ uint32_t kv4_max_u16x2(uint32_t a, uint32_t b) {
     return d;
 }
 
+// Index of a token's item `at` of a head, where a token and head have `per` items (words of codes, steps).  One
+// 64-bit product: the rest stays below 2^22 (1024 heads, pages of 128 tokens, 16 words).
+__device__ __forceinline__ int64_t kv4_cell(const Kv4View& c, int sh, int slot, int head, uint32_t per, uint32_t at) {
+    const uint32_t in = (static_cast<uint32_t>(head) << sh) + (slot & (c.page - 1));
+    return static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(slot >> sh)) * ((static_cast<uint32_t>(c.heads) << sh) * per) +
+                                (in * per + at));
+}
+
 constexpr int kKvBlock = 256;
 constexpr int kKvItems = 4;                        // gather: 8-channel words per thread of large batches, loaded together
 
 // How blocks cover the words (or pairs of words) of n tokens of k (blockIdx.y = 0) or v (1): `tokens` whole tokens per block, or
 // one token in `parts` blocks when it has more words than a block takes.
 struct Kv4Span {
-    int64_t n;
+    uint32_t n;
     int row;                 // words of a token
     uint32_t inv;            // floor(2^32 / row) + 1: quotients of indexes below 2^16 by a multiply
     int tokens, parts, span; // span: words of a block
 };
 // Word `i` of this thread: its token, and the word inside the token; false past the end.
-__device__ __forceinline__ bool kv4_word(const Kv4Span& s, int i, int64_t& tok, int& rest) {
+__device__ __forceinline__ bool kv4_word(const Kv4Span& s, int i, uint32_t& tok, int& rest) {
     const uint32_t li = threadIdx.x + kKvBlock * i;
     if (s.parts > 1) {
-        tok = blockIdx.x / s.parts;
+        tok = blockIdx.x / static_cast<uint32_t>(s.parts);
         rest = static_cast<int>(blockIdx.x - tok * s.parts) * s.span + static_cast<int>(li);
         return rest < s.row;
     }
     const uint32_t t = __umulhi(li, s.inv);
     rest = static_cast<int>(li - t * s.row);
-    tok = static_cast<int64_t>(blockIdx.x) * s.tokens + t;
+    tok = blockIdx.x * static_cast<uint32_t>(s.tokens) + t;             // below 2^31 + 2^13
     return static_cast<int>(t) < s.tokens && tok < s.n;
 }
 
@@ -303,19 +311,19 @@ kv4_append_kernel(const Kv4View c, const Kv4Span s, const void* k, const void* v
     constexpr int kRaw = (BF16 ? 1 : 2) * W;                          // 16-byte loads per unit of W words
     const bool isv = blockIdx.y != 0;
     const char* const src = static_cast<const char*>(isv ? v : k);
-    const int64_t stride = (isv ? v_stride : k_stride) * (BF16 ? 2 : 4);
+    const uint32_t stride = static_cast<uint32_t>((isv ? v_stride : k_stride) / (BF16 ? 8 : 4));     // in 16 bytes
     const int lu = (c.dim == 128 ? 4 : 3) - (W == 2 ? 1 : 0), sh = __ffs(c.page) - 1;      // log2 of units per head
     uint4 raw[ITEMS][kRaw];
     int slot[ITEMS], at[ITEMS];
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-        int64_t tok;
+        uint32_t tok;
         slot[i] = -1;
 #pragma unroll
         for (int h = 0; h < kRaw; ++h) raw[i][h] = make_uint4(0u, 0u, 0u, 0u);
         if (kv4_word(s, i, tok, at[i])) {
             // the values do not wait for the slot (rows without one are read for nothing)
-            const uint4* a = reinterpret_cast<const uint4*>(src + tok * stride) + at[i] * kRaw;
+            const uint4* a = reinterpret_cast<const uint4*>(src) + (static_cast<uint64_t>(tok) * stride + static_cast<uint32_t>(at[i] * kRaw));
 #pragma unroll
             for (int h = 0; h < kRaw; ++h) raw[i][h] = __ldcs(a + h);
             slot[i] = kv4_ld(slots + tok);
@@ -386,12 +394,11 @@ kv4_append_kernel(const Kv4View c, const Kv4Span s, const void* k, const void* v
                                         make_float4(x[w][4], x[w][5], x[w][6], x[w][7]), step);
         }
         const int head = at[i] >> lu, u = at[i] & ((1 << lu) - 1);
-        const int64_t cell = (static_cast<int64_t>(slot[i] >> sh) * c.heads + head) * c.page + (slot[i] & (c.page - 1));
-        uint32_t* to = reinterpret_cast<uint32_t*>(isv ? c.vc : c.kc) + ((cell << lu) + u) * W;
+        uint32_t* to = reinterpret_cast<uint32_t*>(isv ? c.vc : c.kc) + kv4_cell(c, sh, slot[i], head, W << lu, u * W);
         if (W == 2) *reinterpret_cast<uint2*>(to) = make_uint2(word[0], word[W - 1]);
         else *to = word[0];
         if ((u & (4 / W - 1)) == 0)
-            (isv ? c.vs : c.ks)[(cell << (lu - (W == 2 ? 1 : 2))) + u / (4 / W)] = static_cast<uint16_t>(__float_as_uint(step) >> 16);
+            (isv ? c.vs : c.ks)[kv4_cell(c, sh, slot[i], head, (W << lu) / 4, u / (4 / W))] = static_cast<uint16_t>(__float_as_uint(step) >> 16);
     }
 }
 
@@ -428,18 +435,17 @@ kv4_gather_kernel(const Kv4View c, const Kv4Span s, const int* slots, uint16_t* 
     int64_t to[ITEMS];
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-        int64_t tok;
+        uint32_t tok;
         int rest;
         to[i] = -1;
         q[i] = st[i] = 0;
         if (!kv4_word(s, i, tok, rest)) continue;
-        to[i] = tok * s.row + rest;
+        to[i] = static_cast<int64_t>(static_cast<uint64_t>(tok) * static_cast<uint32_t>(s.row)) + rest;
         const int slot = kv4_ld(slots + tok);
         if (slot < 0 || (slot >> sh) >= c.pages) continue;
         const int head = rest >> lw, w = rest & ((1 << lw) - 1);
-        const int64_t cell = (static_cast<int64_t>(slot >> sh) * c.heads + head) * c.page + (slot & (c.page - 1));
-        q[i] = codes[(cell << lw) + w];
-        st[i] = steps[(cell << (lw - 2)) + (w >> 2)];
+        q[i] = codes[kv4_cell(c, sh, slot, head, 1u << lw, w)];
+        st[i] = steps[kv4_cell(c, sh, slot, head, 1u << (lw - 2), w >> 2)];
     }
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {

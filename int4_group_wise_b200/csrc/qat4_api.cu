@@ -873,7 +873,7 @@ static qat4::Kv4View kv4_view(const qat4_kv4_cache* c) {
 static bool kv4_many(int64_t n, int64_t row, int64_t least) { return n * row >= least * 148 * qat4::kKvBlock; }
 static qat4::Kv4Span kv4_span(int64_t n, int64_t row, int items, dim3* grid) {
     qat4::Kv4Span s;
-    s.n = n;
+    s.n = static_cast<uint32_t>(n);
     s.row = static_cast<int>(row);
     s.inv = static_cast<uint32_t>((uint64_t(1) << 32) / static_cast<uint64_t>(row)) + 1;
     s.span = qat4::kKvBlock * items;
