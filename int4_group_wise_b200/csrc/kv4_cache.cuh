@@ -299,9 +299,9 @@ __device__ __forceinline__ bool kv4_word(const Kv4Span& s, int i, uint32_t& tok,
 
 // Thread = W words of 8 channels of a token and head, ITEMS times; 4 / W neighbouring lanes hold a group and find
 // its largest magnitude by shuffles.  One pass: each value is read once, a thread's codes leave in one store.
-// Bound: HBM.  16411 tokens of 8 heads of 128 (67 MB in, 19 MB out, 13.4 us at the copy rate) take 17.2 us with two
-// times two words a thread (18.4 with one time two, 25.6 with one word: half the bytes in flight per thread, and
-// twice the work on steps).
+// Bound: HBM, with the issue slots 70% busy.  16411 tokens of 8 heads of 128 (67 MB in, 19 MB out, 13.4 us at the
+// copy rate), columns of a stacked projection, take 17.3 us with two times two words a thread; with 64-bit
+// indexes throughout it was 17.9, and one time two words 18.4, two times one 22.9, four times two 19.2.
 template <bool BF16, int ITEMS, int W>
 __global__ void __launch_bounds__(kKvBlock)
 kv4_append_kernel(const Kv4View c, const Kv4Span s, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
@@ -421,7 +421,7 @@ __device__ __forceinline__ uint32_t kv4_off(uint32_t step2) {
 
 // Thread = 8 channels of a token and head, ITEMS of them at a time: 4 bytes of codes in, 16 bytes out; rows
 // without a slot are zero.  Bound: HBM (19 MB in and 67 MB out for 16411 tokens of 8 heads of 128: 13.4 us at the
-// copy rate, 16.3 measured).
+// copy rate, 13.8 measured).
 template <int ITEMS>
 __global__ void __launch_bounds__(kKvBlock)
 kv4_gather_kernel(const Kv4View c, const Kv4Span s, const int* slots, uint16_t* k, uint16_t* v) {

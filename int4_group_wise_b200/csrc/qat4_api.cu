@@ -867,9 +867,9 @@ static qat4::Kv4View kv4_view(const qat4_kv4_cache* c) {
 // Blocks over the units (8 or 16 channels) of n tokens of k and v: `row` units a token, at least 4 and at most 16384;
 // `items` units per thread.
 // Large batches, of `least` words and more for every thread of a block on each SM, take several words per thread.
-// Tokens of 8 heads of 128, one word a thread and several, us: append bf16 1184: 2.7, 3.8; 2400: 5.1, 4.4; 16411:
-// 25.6, 17.2.  append float32 2400: 5.5, 6.0; 4800: 9.3, 9.6; 16411: 27.5, 24.8.  gather 2400: 3.8, 5.0; 4800: 6.7,
-// 5.6; 16411: 19.1, 15.4.
+// Tokens of 8 heads of 128, one word a thread and several, us: append bf16 1184: 2.7, 3.7; 2400: 5.0, 4.3; 16411:
+// 24.3, 16.6.  append float32 2400: 5.4, 5.9; 4800: 9.1, 9.5; 16411: 26.8, 24.7.  gather 2400: 3.7, 4.6; 4800: 6.5,
+// 5.3; 16411: 18.7, 13.9.
 static bool kv4_many(int64_t n, int64_t row, int64_t least) { return n * row >= least * 148 * qat4::kKvBlock; }
 static qat4::Kv4Span kv4_span(int64_t n, int64_t row, int items, dim3* grid) {
     qat4::Kv4Span s;
