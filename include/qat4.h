@@ -370,8 +370,9 @@ qat4_status qat4_fq_gemm_staged(const uint16_t *X, int64_t T, const float *W, co
  *            head_dim / 32]: one step size per 32 channels, as
  *            qat4_kv4_append writes them: 5 significant bits, 0 or between
  *            2^-100 and 2^100, so that step * code is exactly a bf16.  The
- *            attention and gather calls round step * code of other steps to
- *            bf16; steps that are negative, infinite or NaN give unspecified
+ *            attention and gather calls take other steps too, any bf16 from 0
+ *            to 2^100, and round step * code to bf16 (once, to nearest even);
+ *            steps that are negative, larger, infinite or NaN give unspecified
  *            values (never a fault).
  *  page_size 16, 32, 64 or 128;  head_dim 64 or 128;  1 <= kv_heads <= 1024;
  *  num_pages >= 1, num_pages * page_size <= 2^31 - 1.  All four pointers 16-byte

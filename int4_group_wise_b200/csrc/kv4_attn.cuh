@@ -12,8 +12,8 @@
 // Bound: HBM.  A cached token of a head costs 2 * (D/2 + D/16) bytes (144 at
 // D = 128) and 4 * D * rows flop, far below the tensor cores' balance, so the
 // contractions run on mma.sync (m16n8k16) only to keep the issue slots for the
-// decoding: per pair of codes one shift, one logic op and one packed FMA
-// (kv4_pair).  The rows are the MMA's narrow side, and the operand orders are
+// decoding: per pair of codes a shift (for three of four), a logic op, a packed
+// subtraction and a packed product (kv4_pair).  The rows are the MMA's narrow side, and the operand orders are
 // chosen so that the packed words need no reordering:
 //   S^T = K Q^T: A = 16 tokens.  Thread (g, t) holds tokens g and g + 8 and their
 //     channels [32t, 32t + 32) (D = 128): 16 bytes of codes and one step each;
@@ -499,7 +499,7 @@ kv4_decode_kernel(const AttnParams p) {
                 const uint32_t sbase = sb + 2 * L::kCodes + (32 * warp + g) * (D / 32) * 2 + 2 * (t * kW / 4);
 #pragma unroll
                 for (int k = 0; k < kPass; ++k) {
-                    uint32_t w[2][kW], s2[2], o2[2];                 // tokens g and g + 8 of the tile
+                    uint32_t w[2][kW], s2[2];                 // tokens g and g + 8 of the tile
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (kW == 4) {
@@ -510,17 +510,16 @@ kv4_decode_kernel(const AttnParams p) {
                             w[h][0] = x.x; w[h][1] = x.y;
                         }
                         s2[h] = __byte_perm(lds_u16(sbase + (16 * (k0 + k) + 8 * h) * (D / 32) * 2), 0u, 0x1010);
-                        o2[h] = kv4_off(s2[h]);
                     }
 #pragma unroll
                     for (int i = 0; i < kW; ++i) {
                         uint32_t a[2][4];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            a[0][h] = kv4_pair(w[h][i] << 3, s2[h], o2[h]);
-                            a[0][2 + h] = kv4_pair(w[h][i] >> 1, s2[h], o2[h]);
-                            a[1][h] = kv4_pair(w[h][i] >> 5, s2[h], o2[h]);
-                            a[1][2 + h] = kv4_pair(w[h][i] >> 9, s2[h], o2[h]);
+                            a[0][h] = kv4_pair<0>(w[h][i], s2[h]);
+                            a[0][2 + h] = kv4_pair<1>(w[h][i], s2[h]);
+                            a[1][h] = kv4_pair<2>(w[h][i], s2[h]);
+                            a[1][2 + h] = kv4_pair<3>(w[h][i], s2[h]);
                         }
 #pragma unroll
                         for (int n = 0; n < kN; ++n) {
@@ -632,18 +631,17 @@ kv4_decode_kernel(const AttnParams p) {
                         uint32_t s2 = __byte_perm(lds_u16(ss), lds_u16(ss + (D / 32) * 2), 0x5410);
                         if (live != 0xffffffffu)               // tokens that do not exist: step 0
                             s2 &= (((live >> off) & 1u) ? 0xffffu : 0u) | (((live >> (off + 1)) & 1u) ? 0xffff0000u : 0u);
-                        const uint32_t o2 = kv4_off(s2);
 #pragma unroll
                         for (int i = 0; i < kVW; ++i) {
                             const uint32_t lo = __byte_perm(wa[i], wb[i], 0x5410), hi = __byte_perm(wa[i], wb[i], 0x7632);
-                            v[h][8 * i + 0] = kv4_pair(lo << 3, s2, o2);
-                            v[h][8 * i + 1] = kv4_pair(lo >> 1, s2, o2);
-                            v[h][8 * i + 2] = kv4_pair(lo >> 5, s2, o2);
-                            v[h][8 * i + 3] = kv4_pair(lo >> 9, s2, o2);
-                            v[h][8 * i + 4] = kv4_pair(hi << 3, s2, o2);
-                            v[h][8 * i + 5] = kv4_pair(hi >> 1, s2, o2);
-                            v[h][8 * i + 6] = kv4_pair(hi >> 5, s2, o2);
-                            v[h][8 * i + 7] = kv4_pair(hi >> 9, s2, o2);
+                            v[h][8 * i + 0] = kv4_pair<0>(lo, s2);
+                            v[h][8 * i + 1] = kv4_pair<1>(lo, s2);
+                            v[h][8 * i + 2] = kv4_pair<2>(lo, s2);
+                            v[h][8 * i + 3] = kv4_pair<3>(lo, s2);
+                            v[h][8 * i + 4] = kv4_pair<0>(hi, s2);
+                            v[h][8 * i + 5] = kv4_pair<1>(hi, s2);
+                            v[h][8 * i + 6] = kv4_pair<2>(hi, s2);
+                            v[h][8 * i + 7] = kv4_pair<3>(hi, s2);
                         }
                     }
                     // rows g and g + 8 of tile i: this thread's channels i and i + kM

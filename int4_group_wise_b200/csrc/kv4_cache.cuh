@@ -5,10 +5,11 @@
 // channel-unquantized", section "Quantization Configuration": symmetric INT4,
 // zero-point 0, here with one step per 32 channels of a token's head): codes
 // uint8 [pages, heads, page, D/2] (channel 2j low nibble, 2j+1 high nibble, as
-// the W4A16 export), steps bf16 [pages, heads, page, D/32].  A step has 5
-// significant bits, so code * step (3 + 5 bits) is exactly a bf16: the
-// attention kernels feed the tensor cores with the cache's exact values.  The
-// step is fl(m / 7) rounded UP to those 5 bits (m the group's largest
+// the W4A16 export), steps bf16 [pages, heads, page, D/32].  A step that
+// append writes has 5 significant bits, so code * step (3 + 5 bits) is exactly a
+// bf16: the attention kernels feed the tensor cores with the cache's exact
+// values.  Steps of other makers may have all 8 bits; their code * step is
+// rounded to bf16 once.  The step is fl(m / 7) rounded UP to those 5 bits (m the group's largest
 // magnitude), so no code is clipped; against an unrounded step the grid is up
 // to 1/16 (on average 1/32) coarser.
 #pragma once
@@ -198,7 +199,7 @@ kv4_tables_kernel(const TablesParams p) {
 // Step of a group from its largest magnitude: fl(m / 7) with the 19 low of its
 // 23 stored significand bits rounded up (the carry moves into the exponent), at
 // most 2^100, and 0 below 2^-100 (then every code is 0).  The limits keep the
-// step, its reciprocal and 24 * step away from overflow and subnormals.
+// step and its reciprocal away from overflow and subnormals.
 __device__ __forceinline__ float kv4_step(float m) {
     const float d = __fdiv_rn(m, 7.0f);
     const float up = __uint_as_float((__float_as_uint(d) + 0x7FFFFu) & ~0x7FFFFu);
@@ -403,19 +404,20 @@ kv4_append_kernel(const Kv4View c, const Kv4Span s, const void* k, const void* v
 }
 
 // ------------------------------------------------------------------ gather
-// Two bf16 values code * step from nibbles at bits 3..6 and 19..22 of v: one logic op
-// flips the nibble's top bit and puts it under the exponent of 16 (16 + (code + 8)); one packed FMA
-// with (step, -24 * step) leaves code * step.  Exact for steps of at most 5 significant bits.
-__device__ __forceinline__ uint32_t kv4_pair(uint32_t v, uint32_t step2, uint32_t off2) {
-    uint32_t x, r;
-    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(x) : "r"(v), "r"(0x00780078u), "r"(0x41C041C0u));
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(step2), "r"(off2));
-    return r;
-}
-// -24 * step for a pair of steps (two products, one rounding each, exact for 5-bit steps).
-__device__ __forceinline__ uint32_t kv4_off(uint32_t step2) {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(step2), "r"(0xC1C0C1C0u));
+// Two bf16 values code * step from nibbles K and K + 4 of a word: a shift (none for K = 0), one logic op that
+// flips the nibble's top bit and puts it into the significand of 16 (16 + (code + 8); K = 0: of 128), a packed
+// subtraction that leaves the code exactly, and a packed product, rounded once, whatever the step.  Taking the
+// offset off inside the product, fma(x, step, -24 step), saves the subtraction but is right for steps of at most 6
+// significant bits only (3 step has to fit a bf16): it was 3% faster in the decode kernel (64 ragged requests 95 us
+// for 97.6); looking at the steps first, to choose between the two, cost as much as the subtraction.
+template <int K>
+__device__ __forceinline__ uint32_t kv4_pair(uint32_t w, uint32_t step2) {
+    const uint32_t v = K == 0 ? w : w >> (4 * K - 3);
+    constexpr uint32_t kMask = K == 0 ? 0x000F000Fu : 0x00780078u, kZero = K == 0 ? 0x43084308u : 0x41C041C0u;
+    uint32_t x, c, r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(x) : "r"(v), "r"(kMask), "r"(kZero));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(x), "r"(kZero));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(c), "r"(step2));
     return r;
 }
 
@@ -450,9 +452,9 @@ kv4_gather_kernel(const Kv4View c, const Kv4Span s, const int* slots, uint16_t* 
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
         if (to[i] < 0) continue;
-        const uint32_t s2 = st[i] | (st[i] << 16), o2 = kv4_off(s2);
-        const uint32_t a = kv4_pair(q[i] << 3, s2, o2), b = kv4_pair(q[i] >> 1, s2, o2);      // channels (0, 4), (1, 5)
-        const uint32_t e = kv4_pair(q[i] >> 5, s2, o2), f = kv4_pair(q[i] >> 9, s2, o2);      // (2, 6), (3, 7)
+        const uint32_t s2 = st[i] | (st[i] << 16);
+        const uint32_t a = kv4_pair<0>(q[i], s2), b = kv4_pair<1>(q[i], s2);      // channels (0, 4), (1, 5)
+        const uint32_t e = kv4_pair<2>(q[i], s2), f = kv4_pair<3>(q[i], s2);      // (2, 6), (3, 7)
         __stcs(reinterpret_cast<uint4*>(isv ? v : k) + to[i],
                make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(e, f, 0x5410), __byte_perm(a, b, 0x7632), __byte_perm(e, f, 0x7632)));
     }
