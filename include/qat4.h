@@ -316,6 +316,10 @@ qat4_status qat4_refine(const float *W, int64_t R, int64_t C, const float *H, in
  *  y       out float32 [M, R]; zeroed on the stream first, then written.  Products are
  *          exact (bf16 codes times bf16 x on the tensor cores), sums float32 in an order
  *          fixed by (R, C, M) and the SM count.
+ *  The codes, which a server does not change, may be read before the kernel ahead of this
+ *  call in the stream has ended, if that kernel launches its dependents early (programmatic
+ *  dependent launch): such a kernel must not write them (this library's writers of packed do
+ *  not launch early).  x, scales and y keep the stream's order whatever comes before.
  *  C must be a multiple of 32 and small enough that one token's x (bf16) and three 16 KB
  *  stages fit the opt-in shared memory of a block (C <= 88064 on B200); else _SHAPE.
  *  Errors: QAT4_ERR_NULL, _SHAPE, _ALIGN, _CUDA. */

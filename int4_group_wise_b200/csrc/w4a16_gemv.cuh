@@ -134,8 +134,8 @@ __device__ __forceinline__ void gm_scales(const GmScaleCtx& x, int b, int ch, fl
     const int q0 = ch * (kGmChunkCols / 32) + kGmQuads * x.warp;   // this warp's first group of 32 columns
     if (x.fast32 && q0 + kGmQuads <= x.G) {
         uint4 va = make_uint4(0u, 0u, 0u, 0u), vb = make_uint4(0u, 0u, 0u, 0u);
-        if (ra < x.R) va = __ldg(reinterpret_cast<const uint4*>(x.scales + static_cast<int64_t>(ra) * x.G + q0));
-        if (rb < x.R) vb = __ldg(reinterpret_cast<const uint4*>(x.scales + static_cast<int64_t>(rb) * x.G + q0));
+        if (ra < x.R) va = *reinterpret_cast<const uint4*>(x.scales + static_cast<int64_t>(ra) * x.G + q0);
+        if (rb < x.R) vb = *reinterpret_cast<const uint4*>(x.scales + static_cast<int64_t>(rb) * x.G + q0);
         const uint32_t a4[4] = {va.x, va.y, va.z, va.w}, b4[4] = {vb.x, vb.y, vb.z, vb.w};
 #pragma unroll
         for (int j = 0; j < kGmQuads; ++j) {
@@ -145,8 +145,8 @@ __device__ __forceinline__ void gm_scales(const GmScaleCtx& x, int b, int ch, fl
         return;
     }
     if (x.G == 1) {
-        const float sa = ra < x.R ? __half2float(__ushort_as_half(__ldg(x.scales + ra))) : 0.0f;
-        const float sb = rb < x.R ? __half2float(__ushort_as_half(__ldg(x.scales + rb))) : 0.0f;
+        const float sa = ra < x.R ? __half2float(__ushort_as_half(x.scales[ra])) : 0.0f;
+        const float sb = rb < x.R ? __half2float(__ushort_as_half(x.scales[rb])) : 0.0f;
 #pragma unroll
         for (int j = 0; j < kGmQuads; ++j) { s[2 * j] = sa; s[2 * j + 1] = sb; }
         return;
@@ -157,9 +157,9 @@ __device__ __forceinline__ void gm_scales(const GmScaleCtx& x, int b, int ch, fl
         const bool in = c < x.C;
         const int gi = in ? c / x.group : 0;
         s[2 * j] = (in && ra < x.R)
-                       ? __half2float(__ushort_as_half(__ldg(x.scales + static_cast<int64_t>(ra) * x.G + gi))) : 0.0f;
+                       ? __half2float(__ushort_as_half(x.scales[static_cast<int64_t>(ra) * x.G + gi])) : 0.0f;
         s[2 * j + 1] = (in && rb < x.R)
-                           ? __half2float(__ushort_as_half(__ldg(x.scales + static_cast<int64_t>(rb) * x.G + gi))) : 0.0f;
+                           ? __half2float(__ushort_as_half(x.scales[static_cast<int64_t>(rb) * x.G + gi])) : 0.0f;
     }
 }
 
@@ -168,7 +168,10 @@ __device__ __forceinline__ void gm_scales(const GmScaleCtx& x, int b, int ch, fl
 // the next kernel may start while this one finishes: the next call's CTAs
 // become resident as this one's retire and start streaming their (constant)
 // codes, and wait for this kernel's completion only before they read x or
-// touch y.
+// touch y.  The kernel before may be one that launches its dependents on its
+// first line (the attention that writes x), so x and the scales are read by
+// plain loads: the read-only path supposes data that no one writes while the
+// kernel lives, and this kernel may live while x is being written.
 
 // Zeroes y (the row blocks cut between two CTAs get two atomic partials), in
 // order: it may start early, but writes y only after the previous kernel of
@@ -263,14 +266,25 @@ w4a16_gemv_kernel(const __grid_constant__ CUtensorMap tmap, const GemvParams p) 
     // stage x once: token m's word w (columns 8w..8w+7) in the order 0,4,1,5,2,6,3,7; columns
     // past C are zero
     {
-        const int words = (p.xstride - 64) / 16;
-        for (int u = threadIdx.x; u < p.MT * words; u += 32 * kGmWarps) {
-            const int m = u / words, w = u - m * words;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (w * 8 < p.C) v = __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(m) * p.C + w * 8));
-            const uint4 o = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                                       __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-            *reinterpret_cast<uint4*>(smem + (xs - ring) + m * p.xstride + w * 16) = o;
+        // four loads in flight (plain loads stay behind the stores before them; one at a time, one to six tokens of
+        // 4096 x 14336 took 1-2% longer)
+        const int words = (p.xstride - 64) / 16, all = p.MT * words;
+        for (int u0 = threadIdx.x; u0 < all; u0 += 4 * 32 * kGmWarps) {
+            uint4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int u = u0 + 32 * kGmWarps * i, m = u / words, w = u - m * words;
+                v[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (u < all && w * 8 < p.C) v[i] = *reinterpret_cast<const uint4*>(p.x + static_cast<int64_t>(m) * p.C + w * 8);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int u = u0 + 32 * kGmWarps * i, m = u / words, w = u - m * words;
+                if (u < all)
+                    *reinterpret_cast<uint4*>(smem + (xs - ring) + m * p.xstride + w * 16) =
+                        make_uint4(__byte_perm(v[i].x, v[i].z, 0x5410), __byte_perm(v[i].x, v[i].z, 0x7632),
+                                   __byte_perm(v[i].y, v[i].w, 0x5410), __byte_perm(v[i].y, v[i].w, 0x7632));
+            }
         }
         asm volatile("bar.sync 1, %0;" :: "n"(32 * kGmWarps) : "memory");
     }
