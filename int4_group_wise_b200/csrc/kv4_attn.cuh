@@ -244,10 +244,13 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t a) {
 // the cluster's shared memory: one launch and no workspace, for batches too small to fill the GPU.
 // Otherwise the stream of all units is cut evenly over the grid.
 constexpr int kKaCluster = 8;
+// Tiles that come in clusters: batches with tiles of 24 rows fill the GPU.
+__host__ __device__ constexpr bool ka_clusters(int rows) { return rows < 24; }
 
 template <int D, int ROWS, bool CL>
 __global__ void __launch_bounds__(kKaThreads, KaLayout<D, ROWS>::kPerSm)
 kv4_decode_kernel(const AttnParams p) {
+    static_assert(!CL || ka_clusters(ROWS), "no call has clusters of such tiles");
     using L = KaLayout<D, ROWS>;
     constexpr int kStages = L::kStages;
     constexpr bool kLo = ROWS == 4;            // columns 4..7 carry the weights' rounding remainders

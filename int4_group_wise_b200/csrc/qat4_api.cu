@@ -930,8 +930,10 @@ static bool smem_attr(K kernel, size_t bytes) {
 
 template <int D, int ROWS>
 static bool kv4_decode_attr() {
-    return smem_attr(qat4::kv4_decode_kernel<D, ROWS, false>, qat4::KaLayout<D, ROWS>::kSmem) &&
-           smem_attr(qat4::kv4_decode_kernel<D, ROWS, true>, qat4::KaLayout<D, ROWS>::kSmem);
+    if constexpr (qat4::ka_clusters(ROWS)) {
+        if (!smem_attr(qat4::kv4_decode_kernel<D, ROWS, true>, qat4::KaLayout<D, ROWS>::kSmem)) return false;
+    }
+    return smem_attr(qat4::kv4_decode_kernel<D, ROWS, false>, qat4::KaLayout<D, ROWS>::kSmem);
 }
 
 // Shared-memory limits of the cache's kernels, once per context.
@@ -1091,9 +1093,12 @@ static size_t kv4_decode_bytes(int64_t D) {
 // to 24 rows that pays once there are tiles enough to fill the GPU (5 drafted tokens, 32/8 heads of 128: 16
 // requests take 57 us with tiles of 24 rows and 65 with two of 16; four requests 29 and 25); above, a request
 // takes two tiles in any case, and tiles of 16 have the faster kernel.
+static constexpr int64_t kTallTiles = 64;
 static int kv4_tile_rows(int64_t rows, int64_t B, int64_t kv_heads) {
-    return rows <= 4 * B ? 4 : rows <= 8 * B ? 8 : rows > 16 * B && rows <= 24 * B && B * kv_heads >= 64 ? 24 : 16;
+    return rows <= 4 * B ? 4 : rows <= 8 * B ? 8 : rows > 16 * B && rows <= 24 * B && B * kv_heads >= kTallTiles ? 24 : 16;
 }
+// Tiles of 24 rows come in batches that are too many for clusters.
+static_assert(kTallTiles * qat4::kKaCluster > 2 * kKaSms && !qat4::ka_clusters(24), "clusters of 24 rows are not built");
 
 // Clusters of the one-launch form of the decode kernel (upper bound of the row tiles over all kv heads), or 0
 // where the batch fills the GPU, or a request may be longer than four chunks for each CTA of a cluster (one
@@ -1125,9 +1130,11 @@ extern "C" size_t qat4_kv4_attention_workspace_bytes(int64_t N, int64_t B, int64
 template <int D, int ROWS>
 static bool kv4_decode_launch(const qat4::AttnParams& p, int64_t clusters, cudaStream_t stream) {
     using L = qat4::KaLayout<D, ROWS>;
-    if (clusters > 0)
-        return launch_pdl(qat4::kv4_decode_kernel<D, ROWS, true>, dim3(static_cast<unsigned>(clusters * qat4::kKaCluster)),
-                          qat4::kKaThreads, L::kSmem, stream, qat4::kKaCluster, p);
+    if constexpr (qat4::ka_clusters(ROWS)) {
+        if (clusters > 0)
+            return launch_pdl(qat4::kv4_decode_kernel<D, ROWS, true>, dim3(static_cast<unsigned>(clusters * qat4::kKaCluster)),
+                              qat4::kKaThreads, L::kSmem, stream, qat4::kKaCluster, p);
+    }
     const int grid = kKaSms * L::kPerSm;
     return launch_pdl(qat4::kv4_decode_kernel<D, ROWS, false>, dim3(grid), qat4::kKaThreads, L::kSmem, stream, 1, p) &&
            launch_pdl(qat4::kv4_combine_kernel<D, ROWS>, dim3(grid, ROWS / 4), qat4::kKcThreads, 0, stream, 1, p, grid);
