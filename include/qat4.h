@@ -479,7 +479,9 @@ qat4_status qat4_kv4_gather(const qat4_kv4_cache *cache, const int32_t *slots, i
  *            overlap on the GPU (other streams, two captured graphs) need one
  *            each.
  *  Keys and values enter exactly, products are exact, sums and statistics
- *  float32; the softmax weights are rounded to bf16 for the second product
+ *  float32 (the tensor cores' sums over 2^15 tokens at most, then joined, so that
+ *  an output does not lose more than 2^-12 of itself however long the request);
+ *  the softmax weights are rounded to bf16 for the second product
  *  (their sum is not).  The result does not depend on timing (no atomics).
  *  N >= 0; 1 <= B <= 65536; N * q_heads <= 2^31 - 1; max_blocks * page_size <= 2^30.
  *  With cu_q not ascending inside [0, N], rows may be computed twice or not at

@@ -67,6 +67,12 @@ constexpr int kKaWarps = 4;                       // consumer warps
 constexpr int kKaThreads = 32 * (kKaWarps + 1);   // + one producer warp
 constexpr int kKaChunk = 128;                     // tokens per unit
 constexpr float kKaGrow = 8.0f;   // a row's reference maximum moves only when exceeded by 2^8
+// Units after which a tile's rows so far are joined into the CTA's piece in the workspace, and its sums start anew.
+// The tensor cores cut what they add to the bits of the running sum: over n tokens of a warp of like weights the
+// output comes out low by n 2^-27.5 of itself (measured: 4.6e-3 after 2^20 tokens a warp), by 2^-12.5 after the 2^15
+// here (measured: 1.5e-4).
+constexpr int kKaFold = 1024;
+static_assert((kKaFold & (kKaFold - 1)) == 0, "a power of two");
 
 struct AttnParams {
     const uint16_t* q;        // [N, Hq, D], token stride q_stride
@@ -433,6 +439,7 @@ kv4_decode_kernel(const AttnParams p) {
         float m[kN][2], l[kN][2];                   // of rows 8n + 2t and 8n + 2t + 1: reference maximum, sum
         int lim[kN][2], low[kN][2];                 // these rows see the tokens low..lim
         bool fresh = true, dead = false;
+        bool rest = false;                          // the tile's sums before a fold are in its piece
         int seg = 0, seg_c0 = at.ch;
         int s = 0;
         uint32_t ph = 0;
@@ -484,7 +491,7 @@ kv4_decode_kernel(const AttnParams p) {
                         for (int j = 0; j < 4; ++j) acc[i][n][j] = 0.0f;
                 }
                 if (kQs) asm volatile("bar.sync 1, %0;" :: "n"(32 * kKaWarps) : "memory");
-                seg_c0 = at.ch;
+                if (!rest) seg_c0 = at.ch;
                 fresh = false;
             }
             dead = dead || !kv4_wait(&full_bar[s], ph, abort, p.limit_ns);
@@ -662,7 +669,8 @@ kv4_decode_kernel(const AttnParams p) {
             if (++s == kStages) { s = 0; ph ^= 1u; }
 
             const bool tile_end = at.ch == at.un.chunks - 1;
-            if (tile_end || u == u1 - 1) {
+            const bool last = tile_end || u == u1 - 1;
+            if (last || (!CL && ((at.ch - seg_c0) & (kKaFold - 1)) == kKaFold - 1)) {
                 // ---- join the four warps, then write the rows or leave the piece to be joined with others
 #pragma unroll
                 for (int n = 0; n < kN; ++n)
@@ -692,7 +700,7 @@ kv4_decode_kernel(const AttnParams p) {
                     }
                 asm volatile("bar.sync 1, %0;" :: "n"(32 * kKaWarps) : "memory");
                 const int rows = at.r.nq * p.group - at.tile * ROWS;     // rows of this tile that exist
-                const bool whole = !CL && seg_c0 == 0 && tile_end;
+                const bool whole = !CL && seg_c0 == 0 && tile_end;      // no other CTA has keys of this tile
                 const int slot = 2 * static_cast<int>(blockIdx.x) + (seg > 0 ? 1 : 0);
                 float* const piece = CL ? res : p.part + static_cast<int64_t>(slot) * ka_piece<D, ROWS>();
                 constexpr int kPer = D / 8;                             // threads per row: 8 channels each
@@ -712,6 +720,19 @@ kv4_decode_kernel(const AttnParams p) {
                         o[0] += f * a.x; o[1] += f * a.y; o[2] += f * a.z; o[3] += f * a.w;
                         o[4] += f * e.x; o[5] += f * e.y; o[6] += f * e.z; o[7] += f * e.w;
                     }
+                    if (!CL && rest) {
+                        // what an earlier fold left; the row's threads, lanes of one warp, read before one writes
+                        const float m0 = piece[ROWS * D + row], l0 = piece[ROWS * D + ROWS + row];
+                        const float4* src = reinterpret_cast<const float4*>(piece + row * D + d0);
+                        const float4 a = src[0], e = src[1];
+                        __syncwarp(((1u << kPer) - 1u) << (lane & ~(kPer - 1)));
+                        const float top = fmaxf(mm, m0);
+                        const float f = top == -INFINITY ? 0.0f : ex2(mm - top), f0 = top == -INFINITY ? 0.0f : ex2(m0 - top);
+                        mm = top;
+                        ll = f * ll + f0 * l0;
+                        o[0] = f * o[0] + f0 * a.x; o[1] = f * o[1] + f0 * a.y; o[2] = f * o[2] + f0 * a.z; o[3] = f * o[3] + f0 * a.w;
+                        o[4] = f * o[4] + f0 * e.x; o[5] = f * o[5] + f0 * e.y; o[6] = f * o[6] + f0 * e.z; o[7] = f * o[7] + f0 * e.w;
+                    }
                     if (*abort) continue;
                     if (whole) {
                         const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
@@ -730,12 +751,13 @@ kv4_decode_kernel(const AttnParams p) {
                         }
                     }
                 }
-                if (!CL && !whole && tid == 0)
+                if (!CL && last && !whole && tid == 0)
                     p.meta[2 * blockIdx.x + (seg > 0 ? 1 : 0)] =
                         make_int4(at.b, at.kvh * at.un.tiles + at.tile, seg_c0, tile_end ? -(at.ch + 1) : at.ch + 1);
                 asm volatile("bar.sync 1, %0;" :: "n"(32 * kKaWarps) : "memory");
                 fresh = true;
-                ++seg;
+                rest = !last;
+                if (last) ++seg;
             }
             if (u + 1 < u1) at.next(p, true);
         }

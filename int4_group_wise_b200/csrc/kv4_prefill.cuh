@@ -31,6 +31,8 @@
 //
 // With few row tiles the keys of each are cut into `splits` equal parts, which
 // leave (maximum, sum, unnormalised O) in the workspace for kv4_join_kernel.
+// The keys of an item come in parts of kKpFold blocks, one after the other, which
+// the CTA joins in the workspace itself.
 //
 // Measured on a B200 (calls replayed from a graph): a prompt of 4096 tokens with
 // 32/8 heads of 128, 147 us = 935 TFLOP/s; three chunks of 1501 tokens on 4674 to
@@ -63,9 +65,16 @@ struct KpLayout {
     static constexpr uint32_t kO = 256;                            // TMEM columns
 };
 
+// Blocks of keys after which a work item is cut, the rows so far wait in the workspace, and O starts anew.  The tensor
+// core cuts what it adds to the bits of the running sum: over n keys of like weights O comes out low by n 2^-27 of
+// itself (measured: 7e-4 after 2^17 keys, 6.5e-3 after 2^20), by 2^-12 after the 2^15 keys here (1.5e-4).  The cut is
+// between items, outside the steps' loop: folding O inside the loop took a prompt of 4096 tokens from 147 to 162 us.
+constexpr int kKpFold = 256;
+
 struct PrefillParams {
     AttnParams a;
-    float* part;             // workspace: [splits][N * Hq][D], then maxima and sums [splits][N * Hq] each
+    float* part;             // workspace: [splits][N * Hq][D], then maxima and sums [splits][N * Hq] each; null where
+                             // splits is 1 and no request can have more than kKpFold blocks
     int splits;
 };
 
@@ -189,7 +198,9 @@ struct KpItem {
     int b, kvh, row0, rows;   // request, kv head, first row and rows of the request
     int q0, len, first, lo;   // of the request (see Request)
     int t_first, n, split;    // first key, blocks of 128 keys
+    int cut;                  // kKpRest: the rows' keys before these are in the workspace; kKpMore: others follow
 };
+enum : int { kKpRest = 1, kKpMore = 2 };
 
 constexpr int kKpGroups = 2048;                    // 32 requests each
 // Row tiles before each 32 requests, and all of them (`groups` + 1 entries), by a converged warp.
@@ -333,7 +344,7 @@ kv4_prefill_kernel(const PrefillParams pp) {
         uint32_t cnt = 0;                                  // 64-key steps of this tile so far
         // the item before, whose rows are still in TMEM
         bool held = false, held_in = false;
-        int held_n = 0, held_split = 0;
+        int held_n = 0, held_split = 0, held_cut = 0;
         int64_t held_at = 0;
         float m = -INFINITY, l = 0.0f;
         for (uint32_t k = 0;; ++k) {
@@ -372,8 +383,22 @@ kv4_prefill_kernel(const PrefillParams pp) {
                     if (!wait(&o_full[x][(cnt - 1) & 1u], (cnt - 1) >> 1)) break;
                     tc_fence_after();
                 }
-                const bool whole = pp.splits == 1;
-                const float f = !whole ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+                const bool whole = pp.splits == 1 && (held_cut & kKpMore) == 0;
+                float* const piece = pp.part + (held_split * all + held_at) * D;
+                float* const st = pp.part + pp.splits * all * D + held_split * all + held_at;
+                float fo = 1.0f, fp = 0.0f;                // of O and of what is in the workspace
+                if ((held_cut & kKpRest) && held_in) {
+                    const float m0 = st[0], top = fmaxf(m, m0);
+                    fo = top == -INFINITY ? 0.0f : ex2(m - top);
+                    fp = top == -INFINITY ? 0.0f : ex2(m0 - top);
+                    m = top;
+                    l = fo * l + fp * st[pp.splits * all];
+                }
+                if (whole) {
+                    const float f = l > 0.0f ? 1.0f / l : 0.0f;
+                    fo *= f;
+                    fp *= f;
+                }
 #pragma unroll 1
                 for (int q = 0; q < D / 32; ++q) {
                     uint32_t o[32];
@@ -388,7 +413,11 @@ kv4_prefill_kernel(const PrefillParams pp) {
                     float v[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i)           // column 8w + (0..7) holds channel 8w + (0, 4, 1, 5, 2, 6, 3, 7)
-                        v[(i & ~7) + ((i & 7) >> 1) + 4 * (i & 1)] = __uint_as_float(o[i]) * f;
+                        v[(i & ~7) + ((i & 7) >> 1) + 4 * (i & 1)] = __uint_as_float(o[i]) * fo;
+                    if (held_cut & kKpRest) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = fmaf(fp, piece[32 * q + i], v[i]);
+                    }
                     if (whole) {
                         uint4* dst = reinterpret_cast<uint4*>(p.out + held_at * D + 32 * q);
 #pragma unroll
@@ -396,7 +425,7 @@ kv4_prefill_kernel(const PrefillParams pp) {
                             dst[i] = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
                                                 pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
                     } else {
-                        float4* dst = reinterpret_cast<float4*>(pp.part + (held_split * all + held_at) * D + 32 * q);
+                        float4* dst = reinterpret_cast<float4*>(piece + 32 * q);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
                     }
@@ -405,9 +434,8 @@ kv4_prefill_kernel(const PrefillParams pp) {
                     if (whole) {
                         if (p.lse) p.lse[held_at] = kv4_lse(m, l);
                     } else {
-                        float* st = pp.part + pp.splits * all * D;
-                        st[held_split * all + held_at] = m;
-                        st[(pp.splits + held_split) * all + held_at] = l;
+                        st[0] = m;
+                        st[pp.splits * all] = l;
                     }
                 }
                 held = false;
@@ -512,6 +540,7 @@ kv4_prefill_kernel(const PrefillParams pp) {
             held_in = in;
             held_n = it.n;
             held_split = it.split;
+            held_cut = it.cut;
             held_at = static_cast<int64_t>(it.q0 + tok) * p.Hq + head;
         }
     } else if (warp < 12) {
@@ -658,16 +687,22 @@ kv4_prefill_kernel(const PrefillParams pp) {
                 KpItem it;
                 const bool work = more && kp_locate(pp, s_first, groups, idx, lane, it);
                 if (work || !more) {
-                    if (k > 0) ok = wait(&item_free, k - 1);           // everyone has read the item before
-                    if (!ok) break;
-                    if (lane == 0) {
-                        if (!more) it.state = -1;
-                        s_item = it;
-                        mbar_arrive(&item_full);
+                    const int first = it.t_first, blocks = work ? it.n : 0;
+                    for (int at = 0; at == 0 || at < blocks; at += kKpFold) {
+                        if (k > 0) ok = wait(&item_free, k - 1);       // everyone has read the item before
+                        if (!ok) break;
+                        if (lane == 0) {
+                            it.t_first = first + at * kKpBlock;
+                            it.n = min(kKpFold, blocks - at);
+                            it.cut = (at > 0 ? kKpRest : 0) | (at + kKpFold < blocks ? kKpMore : 0);
+                            if (!more) it.state = -1;
+                            s_item = it;
+                            mbar_arrive(&item_full);
+                        }
+                        __syncwarp();
+                        ++k;
                     }
-                    __syncwarp();
-                    ++k;
-                    if (!more) break;
+                    if (!ok || !more) break;
                     ok = wait(&item_free, k - 1);                      // and wants the next one
                     if (!ok) break;
                 }

@@ -1122,7 +1122,8 @@ extern "C" size_t qat4_kv4_attention_workspace_bytes(int64_t N, int64_t B, int64
     const Kv4Plan pl = kv4_plan(N, B, group, kv_heads);
     size_t bytes = 0;
     if (pl.decode && kv4_clusters(N, B, group, kv_heads, page_size, max_blocks) == 0) bytes += kv4_decode_bytes(head_dim);
-    if (pl.splits > 1)
+    // the prefill kernel's pieces; one of each row where a request may be so long that its items are cut
+    if (pl.splits > 1 || (pl.prefill && max_blocks * page_size > qat4::kKpFold * qat4::kKpBlock))
         bytes += (static_cast<size_t>(pl.splits) * N * q_heads * (head_dim + 2) * 4 + 255) & ~size_t(255);
     return bytes;
 }

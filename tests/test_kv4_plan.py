@@ -19,3 +19,13 @@ def test_tall_tiles_never_come_in_clusters(heads, dim):
     # and the one-launch form, without a workspace, is there for small batches of lower tiles
     assert q4.kv4_attention_workspace_bytes(1, 1, 4, 1, dim, 16, 256) == 0
     assert q4.kv4_attention_workspace_bytes(20, 1, 1, 1, dim, 16, 256) == 0
+
+
+def test_prompts_over_long_tables_have_a_piece_for_every_row():
+    """A request of more than 2^15 tokens has its sums joined in the workspace: room for a row's output, maximum and sum
+    for each head, from the first table that can name that many; without it, none where one launch does."""
+    n, heads, dim = 20000, 32, 128
+    row = n * heads * (dim + 2) * 4
+    for page in (16, 128):
+        short, long = (q4.kv4_attention_workspace_bytes(n, 1, heads, 8, dim, page, (1 << 15) // page + more) for more in (0, 1))
+        assert short == 0 and row <= long < row + 256
