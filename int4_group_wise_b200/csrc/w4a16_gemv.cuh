@@ -232,6 +232,9 @@ w4a16_gemv_kernel(const __grid_constant__ CUtensorMap tmap, const GemvParams p) 
         uint32_t ph = 0;
         for (int t = t0; t < t1; ++t) {
             int ok = 1;
+            // the ring is full: its first slot is released once the consumers go on, after the kernel before this one,
+            // and the bounded wait for that begins there too, however long that kernel takes
+            if (t - t0 == stages) pdl_wait();
             if (lane == 0) ok = mbar_wait(&empty_bar[s], ph ^ 1u, abort, p.limit_ns) ? 1 : 0;
             if (!__shfl_sync(0xffffffffu, ok, 0)) break;
             const int r = b * kGmRows + lane;

@@ -44,3 +44,13 @@ def test_early_kernels_do_not_use_the_read_only_path(name):
         assert not re.search(r"__ldg\w*\s*\(|ld\.global(\.\w+)*\.nc", part)
     for k in early:
         assert not re.search(r"const\s[^,()]*\*\s*__restrict__", k[:k.index("{")])
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_bounded_waits_begin_after_the_kernel_before(name):
+    """A bounded wait for something that comes only once the kernel ahead has ended would count that kernel's time: in a
+    kernel that waits for the one before it, that wait stands before the first bounded one."""
+    for k in _kernels(_code(name)):
+        early, bounded = re.search(r"\bpdl_wait\(\)", k), re.search(r"\b(mbar_wait\w*|kv4_wait)\(", k)
+        if early and bounded:
+            assert early.start() < bounded.start()
