@@ -1053,15 +1053,20 @@ qat4_status qat4_kv4_gather(const qat4_kv4_cache* cache, const int32_t* slots, i
 static constexpr int kKaSms = 148;
 static constexpr int kKaGrid = 3 * kKaSms;       // most CTAs of the decode kernel
 
+// Batches of so many (request, kv head) pairs fill the GPU with the decode kernel's tiles.
+static constexpr int64_t kTallTiles = 64;
+
 // Which kernels serve a call, from what the host knows of it: N query tokens of B requests.
-//   average rows per request and kv head <= kRowsDecode: the decode kernel takes every request (decode steps,
-//   short drafts);
+//   average rows per request and kv head <= most: the decode kernel takes every request (decode steps, short drafts);
 //   more, and one request: the prefill kernel takes it;
-//   more, and several: requests of up to kRowsDecode rows go to the decode kernel, the others to the prefill
-//   kernel.
-// 16 requests of 700..6007 tokens, 32/8 heads of 128: 20 rows each take 57 us in the decode kernel and 68 in the
-// other, 36 rows 97 and 68.
-static constexpr int64_t kRowsDecode = 32;
+//   more, and several: requests of up to `most` rows go to the decode kernel, the others to the prefill kernel.
+// most is 32, and 24 (one tall tile) for heads of 128 in batches that fill the GPU.  32/8 heads, decode and prefill
+// kernel, us: heads of 128, 16 requests of 700..6007 tokens: 24 rows 60, 69; 28 rows 72, 69; 32 rows 72, 69; 36 rows
+// 101, 70; 64 requests of 500..8000: 24 rows 226, 228; 28 rows 298, 227; 4 requests: 28 rows 28, 39; 32 rows 29, 39;
+// one of 60000: 32 rows 64, 65.  Heads of 64, 16 requests: 28 rows 43, 59; 32 rows 43, 59; 36 rows 60, 59.
+static int64_t kv4_most_rows(int64_t B, int64_t kv_heads, int64_t D) {
+    return D == 128 && B * kv_heads >= kTallTiles ? 24 : 32;
+}
 struct Kv4Plan {
     bool decode, prefill;
     int lo_decode, hi_decode, lo_prefill;
@@ -1070,15 +1075,15 @@ struct Kv4Plan {
                           // requests of 36 rows: 92 us without, 69 with two items per SM, 75 with four)
 };
 
-static Kv4Plan kv4_plan(int64_t N, int64_t B, int64_t group, int64_t kv_heads) {
+static Kv4Plan kv4_plan(int64_t N, int64_t B, int64_t group, int64_t kv_heads, int64_t D) {
     Kv4Plan pl = {true, false, 1, 0x7fffffff, 1, 0, 1};
-    const int64_t rows = N * group;
-    if (rows <= kRowsDecode * B) return pl;
+    const int64_t rows = N * group, most = kv4_most_rows(B, kv_heads, D);
+    if (rows <= most * B) return pl;
     pl.prefill = true;
     pl.decode = B > 1;
     if (pl.decode) {
-        pl.hi_decode = static_cast<int>(kRowsDecode);
-        pl.lo_prefill = static_cast<int>(kRowsDecode) + 1;
+        pl.hi_decode = static_cast<int>(most);
+        pl.lo_prefill = static_cast<int>(most) + 1;
     }
     pl.tiles = rows / qat4::kKpRows + std::min(B, rows / pl.lo_prefill);
     pl.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(16, 2 * kKaSms / (pl.tiles * kv_heads))));
@@ -1093,7 +1098,6 @@ static size_t kv4_decode_bytes(int64_t D) {
 // to 24 rows that pays once there are tiles enough to fill the GPU (5 drafted tokens, 32/8 heads of 128: 16
 // requests take 57 us with tiles of 24 rows and 65 with two of 16; four requests 29 and 25); above, a request
 // takes two tiles in any case, and tiles of 16 have the faster kernel.
-static constexpr int64_t kTallTiles = 64;
 static int kv4_tile_rows(int64_t rows, int64_t B, int64_t kv_heads) {
     return rows <= 4 * B ? 4 : rows <= 8 * B ? 8 : rows > 16 * B && rows <= 24 * B && B * kv_heads >= kTallTiles ? 24 : 16;
 }
@@ -1119,7 +1123,7 @@ extern "C" size_t qat4_kv4_attention_workspace_bytes(int64_t N, int64_t B, int64
         max_blocks > (int64_t(1) << 30) / page_size)
         return 0;
     const int64_t group = q_heads / kv_heads;
-    const Kv4Plan pl = kv4_plan(N, B, group, kv_heads);
+    const Kv4Plan pl = kv4_plan(N, B, group, kv_heads, head_dim);
     size_t bytes = 0;
     if (pl.decode && kv4_clusters(N, B, group, kv_heads, page_size, max_blocks) == 0) bytes += kv4_decode_bytes(head_dim);
     // the prefill kernel's pieces; one of each row where a request may be so long that its items are cut
@@ -1210,7 +1214,7 @@ qat4_status qat4_kv4_attention(const uint16_t* q, int64_t q_stride, int64_t N, i
     // generous bound of a wait: 10 s, and 20 us for every 128 tokens that the table can name (the longest wait of
     // a warp is for another tile's item, one or two microseconds per 128 tokens)
     p.limit_ns = 10000000000ull + 20000ull * static_cast<uint64_t>(max_blocks * cache->page_size / 128);
-    const Kv4Plan pl = kv4_plan(N, B, p.group, H);
+    const Kv4Plan pl = kv4_plan(N, B, p.group, H, D);
     const int64_t clusters = pl.decode ? kv4_clusters(N, B, p.group, H, cache->page_size, max_blocks) : 0;
     bool ok = true;
     if (pl.decode) {
