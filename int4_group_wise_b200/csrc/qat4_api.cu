@@ -931,9 +931,10 @@ static bool smem_attr(K kernel, size_t bytes) {
 template <int D, int ROWS>
 static bool kv4_decode_attr() {
     if constexpr (qat4::ka_clusters(ROWS)) {
-        if (!smem_attr(qat4::kv4_decode_kernel<D, ROWS, true>, qat4::KaLayout<D, ROWS>::kSmem)) return false;
+        if (!smem_attr(qat4::kv4_decode_kernel<D, ROWS, true, false>, qat4::KaLayout<D, ROWS>::kSmem)) return false;
     }
-    return smem_attr(qat4::kv4_decode_kernel<D, ROWS, false>, qat4::KaLayout<D, ROWS>::kSmem);
+    return smem_attr(qat4::kv4_decode_kernel<D, ROWS, false, false>, qat4::KaLayout<D, ROWS>::kSmem) &&
+           smem_attr(qat4::kv4_decode_kernel<D, ROWS, false, true>, qat4::KaLayout<D, ROWS>::kSmem);
 }
 
 // Shared-memory limits of the cache's kernels, once per context.
@@ -1137,11 +1138,18 @@ static bool kv4_decode_launch(const qat4::AttnParams& p, int64_t clusters, cudaS
     using L = qat4::KaLayout<D, ROWS>;
     if constexpr (qat4::ka_clusters(ROWS)) {
         if (clusters > 0)
-            return launch_pdl(qat4::kv4_decode_kernel<D, ROWS, true>, dim3(static_cast<unsigned>(clusters * qat4::kKaCluster)),
-                              qat4::kKaThreads, L::kSmem, stream, qat4::kKaCluster, p);
+            return launch_pdl(qat4::kv4_decode_kernel<D, ROWS, true, false>,
+                              dim3(static_cast<unsigned>(clusters * qat4::kKaCluster)), qat4::kKaThreads, L::kSmem, stream,
+                              qat4::kKaCluster, p);
     }
     const int grid = kKaSms * L::kPerSm;
-    return launch_pdl(qat4::kv4_decode_kernel<D, ROWS, false>, dim3(grid), qat4::kKaThreads, L::kSmem, stream, 1, p) &&
+    // most units of the call, cut into `grid` equal ranges
+    const int64_t rows = static_cast<int64_t>(p.N) * p.group, chunk = qat4::kKaChunk;
+    const int64_t chunks = (static_cast<int64_t>(p.max_blocks) * p.c.page + chunk - 1) / chunk;
+    const int64_t tiles = (rows / ROWS + std::min<int64_t>(p.B, rows)) * p.c.heads;
+    const bool fold = tiles > qat4::kKaFold * static_cast<int64_t>(grid) / chunks;
+    return launch_pdl(fold ? qat4::kv4_decode_kernel<D, ROWS, false, true> : qat4::kv4_decode_kernel<D, ROWS, false, false>,
+                      dim3(grid), qat4::kKaThreads, L::kSmem, stream, 1, p) &&
            launch_pdl(qat4::kv4_combine_kernel<D, ROWS>, dim3(grid, ROWS / 4), qat4::kKcThreads, 0, stream, 1, p, grid);
 }
 
