@@ -479,13 +479,15 @@ qat4_status qat4_kv4_gather(const qat4_kv4_cache *cache, const int32_t *slots, i
  *            overlap on the GPU (other streams, two captured graphs) need one
  *            each.
  *  Keys and values enter exactly, products are exact, sums and statistics
- *  float32 (the tensor cores' sums over 2^15 tokens at most, then joined, so that
- *  an output does not lose more than 2^-12 of itself however long the request);
+ *  float32 (the tensor cores' sums, which cut what they add, over 2^15 tokens at
+ *  most and then joined: an output loses 2^-12 of its row's sum of p |v| at most,
+ *  however long the request);
  *  the softmax weights are rounded to bf16 for the second product
  *  (their sum is not).  The result does not depend on timing (no atomics).
  *  N >= 0; 1 <= B <= 65536; N * q_heads <= 2^31 - 1; max_blocks * page_size <= 2^30.
  *  With cu_q not ascending inside [0, N], rows may be computed twice or not at
- *  all; with scale * q.k overflowing float32 the row is unspecified.
+ *  all; with scale * q.k, or 2^8 times the sum of |v| over a row's keys, overflowing
+ *  float32 the row is unspecified.
  *  Errors: QAT4_ERR_NULL, _SHAPE, _ALIGN, _WORKSPACE, _CUDA; a bounded wait that
  *  gives up leaves QAT4_ERR_TIMEOUT for qat4_sync_check. */
 size_t qat4_kv4_attention_workspace_bytes(int64_t N, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim,

@@ -81,3 +81,27 @@ def test_sums_over_millions_of_tokens(batch, nq, tokens, q_heads, dim, growing):
     assert far <= 1.0, far
     noise = 4 * (2.0 ** -8 / math.sqrt(3)) * (math.sqrt(1 / number) + math.sqrt(shares) / (number / dim))
     assert abs(total / number) <= 2.0 ** -11 + noise, (total / number, noise)
+
+
+@pytest.mark.parametrize("batch,nq,tokens,dim", [(500, 1, 1 << 20, 64), (130, 5, 1 << 22, 128), (40, 64, 1 << 18, 64), (2, 300, 1 << 18, 128)])
+def test_joined_sums_of_rows_apart(batch, nq, tokens, dim):
+    """Where sums are joined in the workspace, a request whose table names no page gives zeros, a NaN in a query stays in its
+    row, the other rows keep their bits, and the output may take the queries' place."""
+    q, cache, table, _ = _long(batch, nq, tokens, 4, dim, seed=dim)
+    lens = torch.full((batch,), tokens, dtype=I32, device="cuda")
+    cu = (torch.arange(batch + 1, device="cuda") * nq).to(I32)
+    lse, lse2 = torch.zeros(q.shape[:2], device="cuda"), torch.zeros(q.shape[:2], device="cuda")
+    want = q4.kv4_attention(q, cache, table, lens, cu, lse=lse)
+    dirty, none = q.clone(), table.clone()
+    none[0] = -1
+    dirty[nq + nq // 2, 2, 7] = math.nan
+    got = q4.kv4_attention(dirty, cache, none, lens, cu, lse=lse2)
+    assert not bool(got[:nq].any()) and bool((lse2[:nq] == -math.inf).all())
+    assert bool(torch.isnan(got[nq + nq // 2, 2]).all()) and math.isnan(float(lse2[nq + nq // 2, 2]))
+    got[:nq], lse2[:nq] = want[:nq], lse[:nq]
+    got[nq + nq // 2, 2], lse2[nq + nq // 2, 2] = want[nq + nq // 2, 2], lse[nq + nq // 2, 2]
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16)) and torch.equal(lse2, lse)
+    place = q.clone()
+    q4.kv4_attention(place, cache, table, lens, cu, out=place)
+    q4.sync_check()
+    assert torch.equal(place.view(torch.int16), want.view(torch.int16))
