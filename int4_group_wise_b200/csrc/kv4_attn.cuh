@@ -47,12 +47,14 @@
 // own, joined at the end of a tile's piece.
 //
 // Measured on a B200 (calls replayed from a graph, 32/8 heads of 128): 64 requests
-// of 511 to 8200 tokens, 95 us = 3.4 TB/s (323 MB, 50 us at the copy rate), one of
-// 131,071 tokens 50 us (23), one of 999 in clusters 6.6 us.  What bounds the first is
-// the decoding's instructions: 200 warp instructions per 8 tokens and head, issue
-// slots 61% and the ALU pipe 60% busy; without the copies it takes 89 us, without the
-// arithmetic 58.  Tried and slower: rows on the MMA's wide side (136 us), two CTAs per
-// SM (101), shifts by multiplication (97); four CTAs per SM: the same.
+// of 511 to 8200 tokens, 98 us = 3.3 TB/s (323 MB, 50 us at the copy rate), one of
+// 131,071 tokens 51.5 us (23), one of 999 in clusters 7.0 us.  What bounds the first is
+// latency: 223 warp instructions per 8 tokens and head would take 57 us issued without
+// gaps, but 12 consumer warps a SM, each with one dependent chain from the codes to the
+// second product, fill 66% of the issue slots (ALU pipe 58%, FMA 45%, HBM 51%).  An
+// earlier form with 200 instructions took 95 us, 89 without the copies and 58 without
+// the arithmetic.  Tried on that form and slower: rows on the MMA's wide side (136 us),
+// two CTAs per SM (101), shifts by multiplication (97); four CTAs per SM: the same.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -816,7 +818,7 @@ kv4_decode_kernel(const AttnParams p) {
 // CTA that holds a tile's first piece owns it; the following pieces are the first records of the
 // next CTAs, up to the one that ends the tile.  Four rows per block (blockIdx.y), two warps per row
 // that take every other piece, eight of them in flight (a request over the whole GPU has dozens: one of
-// 131,071 tokens takes 50 us with both kernels, 60 with one piece in flight).
+// 131,071 tokens took 50 us with both kernels, 60 with one piece in flight).
 constexpr int kKcThreads = 256;
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kKcThreads)

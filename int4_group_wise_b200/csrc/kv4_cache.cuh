@@ -56,9 +56,10 @@ struct Kv4View {
 // the tokens, and a second launch would cost more than the scan: 2-3 us), then
 // takes its share of the table rows and of the tokens.  A new token's page is
 // computed from the free list, not read from the table, so no CTA waits for
-// another's writes.  Bound by launch latency up to some ten thousand tokens,
-// then by the 4 bytes written per token: replayed from a graph, 32 requests with
-// one token each take 5.7 us, 1000 requests with 511,000 tokens 8.2.
+// another's writes.  Bound by latency: replayed from a graph, 32 requests
+// with one token each take 6.0 us, of which the launch is about 1.5 and the scan (its
+// divisions by the page size are 64-bit ones) most of the rest; 1000 requests with
+// 511,000 tokens (2 MB written) 8.5.
 constexpr int kTbThreads = 512;
 constexpr int kTbMaxRequests = 16384;
 
@@ -301,8 +302,9 @@ __device__ __forceinline__ bool kv4_word(const Kv4Span& s, int i, uint32_t& tok,
 // Thread = W words of 8 channels of a token and head, ITEMS times; 4 / W neighbouring lanes hold a group and find
 // its largest magnitude by shuffles.  One pass: each value is read once, a thread's codes leave in one store.
 // Bound: HBM, with the issue slots 70% busy.  16411 tokens of 8 heads of 128 (67 MB in, 19 MB out, 13.4 us at the
-// copy rate), columns of a stacked projection, take 17.3 us with two times two words a thread; with 64-bit
-// indexes throughout it was 17.9, and one time two words 18.4, two times one 22.9, four times two 19.2.
+// copy rate), columns of a stacked projection, take 16.4 us with two times two words a thread (17.3 when the
+// variants were measured: with 64-bit indexes throughout 17.9, one time two words 18.4, two times one 22.9, four
+// times two 19.2).
 template <bool BF16, int ITEMS, int W>
 __global__ void __launch_bounds__(kKvBlock)
 kv4_append_kernel(const Kv4View c, const Kv4Span s, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
@@ -423,7 +425,7 @@ __device__ __forceinline__ uint32_t kv4_pair(uint32_t w, uint32_t step2) {
 
 // Thread = 8 channels of a token and head, ITEMS of them at a time: 4 bytes of codes in, 16 bytes out; rows
 // without a slot are zero.  Bound: HBM (19 MB in and 67 MB out for 16411 tokens of 8 heads of 128: 13.4 us at the
-// copy rate, 13.8 measured).
+// copy rate, 13.2 measured).
 template <int ITEMS>
 __global__ void __launch_bounds__(kKvBlock)
 kv4_gather_kernel(const Kv4View c, const Kv4Span s, const int* slots, uint16_t* k, uint16_t* v) {

@@ -35,7 +35,7 @@
 // the CTA joins in the workspace itself.
 //
 // Measured on a B200 (calls replayed from a graph): a prompt of 4096 tokens with
-// 32/8 heads of 128, 147 us = 935 TFLOP/s; three chunks of 1501 tokens on 4674 to
+// 32/8 heads of 128, 149 us = 924 TFLOP/s; three chunks of 1501 tokens on 4674 to
 // 9001 cached ones with heads of 64, 377 us = 612 TFLOP/s.  What bounds it is the
 // round trip of a step (scores, softmax, P, product, and the buffer's next
 // scores), about 2000 clocks of which a thread's exponentials are 512: with them

@@ -867,9 +867,9 @@ static qat4::Kv4View kv4_view(const qat4_kv4_cache* c) {
 // Blocks over the units (8 or 16 channels) of n tokens of k and v: `row` units a token, at least 4 and at most 16384;
 // `items` units per thread.
 // Large batches, of `least` words and more for every thread of a block on each SM, take several words per thread.
-// Tokens of 8 heads of 128, one word a thread and several, us: append bf16 1184: 2.7, 3.7; 2400: 5.0, 4.3; 16411:
-// 24.3, 16.6.  append float32 2400: 5.4, 5.9; 4800: 9.1, 9.5; 16411: 26.8, 24.7.  gather 2400: 3.7, 4.6; 4800: 6.5,
-// 5.3; 16411: 18.7, 13.9.
+// One word a thread and several, us, by words a thread (8 heads of 128; 2 and 8 heads of 64 and 3 of 128 cross at the
+// same places): append bf16 4: 3.2, 3.4; 8: 4.7, 4.0; 12: 6.0, 4.9; 58: 25.2, 17.4.  append float32 8: 5.1, 5.4;
+// 12: 6.5, 6.5; 16: 8.2, 8.0; 58: 27.3, 24.3.  gather 8: 4.0, 4.4; 12: 5.1, 4.9; 16: 6.2, 5.1; 58: 19.3, 14.1.
 static bool kv4_many(int64_t n, int64_t row, int64_t least) { return n * row >= least * 148 * qat4::kKvBlock; }
 static qat4::Kv4Span kv4_span(int64_t n, int64_t row, int items, dim3* grid) {
     qat4::Kv4Span s;
@@ -1107,8 +1107,8 @@ static_assert(kTallTiles * qat4::kKaCluster > 2 * kKaSms && !qat4::ka_clusters(2
 
 // Clusters of the one-launch form of the decode kernel (upper bound of the row tiles over all kv heads), or 0
 // where the batch fills the GPU, or a request may be longer than four chunks for each CTA of a cluster (one
-// request of 999 tokens: 6.6 us against 11.2 with the grid-wide split and its second launch; past that length
-// the split over all SMs wins).
+// request of 999 tokens: 7.0 us against 9.9 with the grid-wide split and its second launch; past that length
+// the split over all SMs wins).  The host knows a request's length by the width of its block table only.
 static int64_t kv4_clusters(int64_t N, int64_t B, int64_t group, int64_t kv_heads, int64_t page, int64_t max_blocks) {
     const int64_t rows = N * group, chunk = qat4::kKaChunk;
     if ((max_blocks * page + chunk - 1) / chunk > 4 * qat4::kKaCluster) return 0;
